@@ -279,6 +279,91 @@ ssd_status_t ssd_gdn_decode_step(float* state, const void* q, const void* k, con
                                  void* stream);
 
 /*
+ * Linear attention with a decay per head: the recurrence of ssd_gdn_decode_step without the
+ * delta correction, and with a decay that belongs to the head instead of the token.  Per
+ * value head h, with g = exp(log_decay[h]) and query/key head h / (heads_v / heads_qk):
+ *     S_t = g S_{t-1} + k_t v_t^T;   o_t = scale * S_t^T q_t           (S: dk x dv, fp32)
+ * ssd_linattn_prefill evaluates it for packed prompts in chunks, ssd_linattn_decode_step
+ * advances the state by one token.  They are the linear layers of a hybrid stack, next to
+ * the softmax layers below, which take the same queries, keys, values and offsets.
+ *
+ * ssd_linattn_prefill: nseq sequences laid end to end, as for ssd_prefill_varlen.
+ *   q, k   [total_tokens][heads_qk][dk] dtype, v [total_tokens][heads_v][dv] dtype, with
+ *          q_stride, k_stride, v_stride elements from one token to the next (multiples of 8
+ *          elements, at least heads x dim): the three may be slices of one fused projection
+ *   log_decay [heads_v] fp32: <= 0 for a contracting state (any value but NaN and +inf is
+ *          computed as given; -inf keeps only the token itself)
+ *   init_states / final_states [nseq][heads_v][dk][dv] fp32; NULL init_states means zeros;
+ *          the two may be the same buffer.  An empty sequence's final state is its initial one.
+ *   cu_seqlens: DEVICE array of nseq + 1 int32 offsets, cu_seqlens[0] = 0, non-decreasing, the
+ *          last at most total_tokens.  Rows of `out` behind the last sequence are left as they
+ *          were.  Offsets that break this record SSD_ERR_SHAPE in the device error word; the
+ *          outputs then mean nothing, but nothing outside the buffers is touched.
+ *   out    [total_tokens][heads_v][dv] dtype (contiguous), rounded once from fp32.
+ * `workspace` holds ssd_linattn_prefill_workspace_bytes(...) bytes of device memory.
+ * Requirements: heads_v % heads_qk == 0; dk and dv multiples of 8 up to 128; heads up to
+ * 65535; nseq in [1, 2^20]; 16-byte aligned pointers (cu_seqlens: 4).  bf16 runs on the
+ * tensor cores, fp32 on the CUDA cores.
+ */
+size_t ssd_linattn_prefill_workspace_bytes(int nseq, int total_tokens, int heads_qk, int heads_v, int dk,
+                                           int dv, ssd_dtype_t dtype);
+ssd_status_t ssd_linattn_prefill(const void* q, const void* k, const void* v, long long q_stride,
+                                 long long k_stride, long long v_stride, const float* log_decay,
+                                 const float* init_states, const int* cu_seqlens, int nseq,
+                                 int total_tokens, int heads_qk, int heads_v, int dk, int dv, float scale,
+                                 ssd_dtype_t dtype, void* out, float* final_states, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
+/*
+ * One token of the same recurrence, in place on the state (one read and one write of it):
+ *   state [batch][heads_v][dk][dv] fp32, in/out;  q, k [batch][heads_qk][dk] dtype;
+ *   v, out [batch][heads_v][dv] dtype;  log_decay [heads_v] fp32.
+ * Requirements as for ssd_linattn_prefill.  The state must not overlap any input or `out`.
+ */
+ssd_status_t ssd_linattn_decode_step(float* state, const void* q, const void* k, const void* v,
+                                     const float* log_decay, int batch, int heads_qk, int heads_v, int dk,
+                                     int dv, float scale, ssd_dtype_t dtype, void* out, void* stream);
+
+/*
+ * Causal softmax attention over packed prompts.  Per query head h, with key/value head
+ * h / (heads_q / heads_kv), for the tokens t of each sequence:
+ *     o_t = sum_{s <= t} softmax_s(scale * q_t . k_s) v_s
+ *   q [total_tokens][heads_q][headdim], k, v [total_tokens][heads_kv][headdim] dtype, token
+ *   strides, cu_seqlens and the rows behind the last sequence as for ssd_linattn_prefill;
+ *   out [total_tokens][heads_q][headdim] dtype (contiguous), rounded once from fp32.
+ * Tokens of one sequence never see another's, whatever values those hold.
+ * Requirements: heads_q % heads_kv == 0; headdim a multiple of 8 up to 128; heads up to
+ * 65535; nseq in [1, 2^20]; 16-byte aligned pointers (cu_seqlens: 4).  bf16 runs on the
+ * tensor cores, fp32 on the CUDA cores.  No workspace.
+ */
+ssd_status_t ssd_attn_prefill(const void* q, const void* k, const void* v, long long q_stride,
+                              long long k_stride, long long v_stride, const int* cu_seqlens, int nseq,
+                              int total_tokens, int heads_q, int heads_kv, int headdim, float scale,
+                              ssd_dtype_t dtype, void* out, void* stream);
+
+/*
+ * One token per sequence against the cache of its sequence:
+ *   k_cache, v_cache [batch][capacity][heads_kv][headdim] dtype, in/out
+ *   cache_lens  DEVICE array [batch] int32: tokens already in each row's cache
+ *   q [batch][heads_q][headdim], k, v [batch][heads_kv][headdim] dtype: the new token
+ *   out [batch][heads_q][headdim] dtype
+ * The new token's k and v are written to row cache_lens[b] of the caches, and the query
+ * attends to rows 0 .. cache_lens[b].  The lengths are not advanced: the caller adds one when
+ * every layer has run.  A negative length marks an unused batch row: its caches and its row
+ * of `out` are left as they were.  A length of `capacity` or more records SSD_ERR_SHAPE in the
+ * device error word, and that row is left as it was.  Cached rows past a length are never read.
+ * `workspace` holds ssd_attn_decode_workspace_bytes(...) bytes of device memory; calls that may
+ * overlap on the GPU need workspaces of their own.  Results do not depend on the order in which
+ * the GPU runs the work.  Requirements as for ssd_attn_prefill; capacity >= 1.
+ */
+size_t ssd_attn_decode_workspace_bytes(int batch, int capacity, int heads_q, int heads_kv, int headdim,
+                                       ssd_dtype_t dtype);
+ssd_status_t ssd_attn_decode_step(void* k_cache, void* v_cache, const int* cache_lens, const void* q,
+                                  const void* k, const void* v, int batch, int capacity, int heads_q,
+                                  int heads_kv, int headdim, float scale, ssd_dtype_t dtype, void* out,
+                                  void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * ssd_prefill without a workspace argument, for callers that may not allocate
  * device memory (a host framework's execution hook that must stay inside the
  * memory it planned, or code running during a CUDA stream capture, where

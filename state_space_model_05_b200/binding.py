@@ -28,6 +28,7 @@ STATUS_NAMES = {0: "SSD_OK", 1: "SSD_ERR_NULL", 2: "SSD_ERR_SHAPE", 3: "SSD_ERR_
 
 # exported symbols and their ctypes signatures, as declared in include/ssd.h
 _P, _I, _Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+_L, _F = ctypes.c_longlong, ctypes.c_float
 SIGNATURES = {
     "ssd_abi_version": ([], _I),
     "ssd_status_string": ([_I], ctypes.c_char_p),
@@ -43,6 +44,13 @@ SIGNATURES = {
     "ssd_prefill_dtraw": ([_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _P, _P, _P, _Z, _P], _I),
     "ssd_decode_step_dtraw": ([_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P], _I),
     "ssd_prefill_noalloc": ([_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _P, _P, _P], _I),
+    "ssd_linattn_prefill_workspace_bytes": ([_I, _I, _I, _I, _I, _I, _I], _Z),
+    "ssd_linattn_prefill": ([_P, _P, _P, _L, _L, _L, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _I, _P, _P, _P, _Z, _P],
+                            _I),
+    "ssd_linattn_decode_step": ([_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _I, _P, _P], _I),
+    "ssd_attn_prefill": ([_P, _P, _P, _L, _L, _L, _P, _I, _I, _I, _I, _I, _F, _I, _P, _P], _I),
+    "ssd_attn_decode_workspace_bytes": ([_I, _I, _I, _I, _I, _I], _Z),
+    "ssd_attn_decode_step": ([_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _I, _P, _P, _Z, _P], _I),
     "ssd_device_status": ([_P], _I),
     "ssd_set_prefill_path": ([_I], _I),
     "ssd_get_prefill_path": ([], _I),
@@ -105,6 +113,10 @@ def _ptr(t):
 def _stream(stream=None):
     s = torch.cuda.current_stream() if stream is None else stream
     return ctypes.c_void_p(s.cuda_stream)
+
+
+def _nbytes(t: torch.Tensor) -> int:
+    return t.numel() * t.element_size()
 
 
 def _need(t: torch.Tensor, name: str, dtype=None):
@@ -340,6 +352,141 @@ def ssd_gdn_decode_step(state, q, k, v, gate, beta, out=None, stream=None):
     return out
 
 
+def _packed(t: torch.Tensor) -> int:
+    """Elements from one token of ``t`` [tokens][heads][dim] to the next, for a tensor whose
+    tokens may lie apart (a slice of a fused projection); each token's own elements may not."""
+    heads, dim = t.shape[1], t.shape[2]
+    if t.numel() and ((dim > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != dim)):
+        raise ValueError("the heads of a token must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else heads * dim
+
+
+def _nseq(cu_seqlens: torch.Tensor) -> int:
+    if cu_seqlens.numel() < 2:
+        raise ValueError("cu_seqlens holds nseq + 1 offsets, at least two")
+    return cu_seqlens.numel() - 1
+
+
+def _check_mixer(ref: torch.Tensor, strided, specs):
+    """_check_args for calls some of whose tensors (``strided``: tensor, name, shape) may have
+    their tokens apart."""
+    for t, name, shape in strided:
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    _check_args(ref, specs)
+    for t, name, _ in strided:
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.dtype != ref.dtype:
+            raise TypeError(f"{name} must be {ref.dtype}")
+        if t.device != ref.device:
+            raise ValueError(f"{name} is on {t.device}, expected {ref.device}")
+
+
+def ssd_linattn_prefill(q, k, v, log_decay, cu_seqlens, scale=1.0, init_states=None, out=None, final_states=None,
+                        workspace=None, stream=None):
+    """Packed linear attention with a decay per head.  q, k [tokens][heads_qk][dk], v
+    [tokens][heads_v][dv] (fp32 or bf16, all alike; tokens may lie apart, as in slices of a fused
+    projection), log_decay [heads_v] fp32, cu_seqlens a CUDA int32 tensor of nseq + 1 offsets.
+    Returns ``(out, final_states)``, out [tokens][heads_v][dv], final_states
+    [nseq][heads_v][dk][dv] fp32; rows of a new ``out`` behind the last sequence are undefined."""
+    _rank(q, "q", "[tokens][heads_qk][dk]")
+    _rank(v, "v", "[tokens][heads_v][dv]")
+    _rank(cu_seqlens, "cu_seqlens", "[nseq + 1]")
+    total, hq, dk = q.shape
+    hv, dv = v.shape[1], v.shape[2]
+    nseq = _nseq(cu_seqlens)
+    f32, state_shape = torch.float32, (nseq, hv, dk, dv)
+    _check_mixer(q, ((q, "q", q.shape), (k, "k", q.shape), (v, "v", (total, hv, dv))),
+                 ((log_decay, "log_decay", (hv,), f32), (cu_seqlens, "cu_seqlens", cu_seqlens.shape, torch.int32),
+                  (init_states, "init_states", state_shape, f32), (out, "out", (total, hv, dv), q.dtype),
+                  (final_states, "final_states", state_shape, f32),
+                  (workspace, "workspace", workspace.shape if workspace is not None else (), None)))
+    code = _dtype_code(q)
+    if out is None:
+        out = torch.empty((total, hv, dv), device=q.device, dtype=q.dtype)
+    if final_states is None:
+        final_states = torch.empty(state_shape, device=q.device, dtype=f32)
+    if workspace is None:
+        need = int(lib().ssd_linattn_prefill_workspace_bytes(nseq, total, hq, hv, dk, dv, code))
+        workspace = torch.empty(max(need, 16), device=q.device, dtype=torch.uint8)
+    st = lib().ssd_linattn_prefill(_ptr(q), _ptr(k), _ptr(v), _packed(q), _packed(k), _packed(v), _ptr(log_decay),
+                                   _ptr(init_states), _ptr(cu_seqlens), nseq, total, hq, hv, dk, dv, scale, code,
+                                   _ptr(out), _ptr(final_states), _ptr(workspace), _nbytes(workspace), _stream(stream))
+    _check(st, "ssd_linattn_prefill")
+    return out, final_states
+
+
+def ssd_linattn_decode_step(state, q, k, v, log_decay, scale=1.0, out=None, stream=None):
+    """One token of linear attention with a decay per head; ``state`` [b][heads_v][dk][dv] fp32 is
+    updated in place.  q, k [b][heads_qk][dk]; v [b][heads_v][dv] (fp32 or bf16, all alike);
+    log_decay [heads_v] fp32.  Returns ``out`` [b][heads_v][dv]."""
+    _rank(q, "q", "[batch][heads_qk][dk]")
+    _rank(v, "v", "[batch][heads_v][dv]")
+    batch, hq, dk = q.shape
+    hv, dv = v.shape[1], v.shape[2]
+    f32 = torch.float32
+    _check_args(q, ((state, "state", (batch, hv, dk, dv), f32), (q, "q", q.shape, q.dtype),
+                    (k, "k", q.shape, q.dtype), (v, "v", (batch, hv, dv), q.dtype),
+                    (log_decay, "log_decay", (hv,), f32), (out, "out", (batch, hv, dv), q.dtype)))
+    if out is None:
+        out = torch.empty_like(v)
+    st = lib().ssd_linattn_decode_step(_ptr(state), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), batch, hq, hv, dk, dv,
+                                       scale, _dtype_code(q), _ptr(out), _stream(stream))
+    _check(st, "ssd_linattn_decode_step")
+    return out
+
+
+def ssd_attn_prefill(q, k, v, cu_seqlens, scale=None, out=None, stream=None):
+    """Causal softmax attention over packed prompts.  q [tokens][heads_q][headdim], k, v
+    [tokens][heads_kv][headdim] (fp32 or bf16, all alike; tokens may lie apart), cu_seqlens a CUDA
+    int32 tensor of nseq + 1 offsets, scale headdim ** -0.5 unless given.  Returns ``out``
+    [tokens][heads_q][headdim]; rows of a new ``out`` behind the last sequence are undefined."""
+    _rank(q, "q", "[tokens][heads_q][headdim]")
+    _rank(k, "k", "[tokens][heads_kv][headdim]")
+    _rank(cu_seqlens, "cu_seqlens", "[nseq + 1]")
+    total, hq, dim = q.shape
+    hkv, nseq = k.shape[1], _nseq(cu_seqlens)
+    _check_mixer(q, ((q, "q", q.shape), (k, "k", (total, hkv, dim)), (v, "v", (total, hkv, dim))),
+                 ((cu_seqlens, "cu_seqlens", cu_seqlens.shape, torch.int32), (out, "out", q.shape, q.dtype)))
+    code = _dtype_code(q)
+    if out is None:
+        out = torch.empty(q.shape, device=q.device, dtype=q.dtype)
+    st = lib().ssd_attn_prefill(_ptr(q), _ptr(k), _ptr(v), _packed(q), _packed(k), _packed(v), _ptr(cu_seqlens),
+                                nseq, total, hq, hkv, dim, dim ** -0.5 if scale is None else scale,
+                                code, _ptr(out), _stream(stream))
+    _check(st, "ssd_attn_prefill")
+    return out
+
+
+def ssd_attn_decode_step(k_cache, v_cache, cache_lens, q, k, v, scale=None, out=None, workspace=None, stream=None):
+    """One token per sequence against its cache: ``k``, ``v`` [b][heads_kv][headdim] join row
+    ``cache_lens[b]`` of k_cache, v_cache [b][capacity][heads_kv][headdim] (in place), and ``q``
+    [b][heads_q][headdim] attends to the rows up to it.  cache_lens: CUDA int32 [b], tokens cached
+    so far (negative: an unused row); it is not advanced.  Returns ``out`` [b][heads_q][headdim];
+    rows of a new ``out`` that belong to unused rows are undefined."""
+    _rank(q, "q", "[batch][heads_q][headdim]")
+    _rank(k_cache, "k_cache", "[batch][capacity][heads_kv][headdim]")
+    batch, hq, dim = q.shape
+    capacity, hkv = k_cache.shape[1], k_cache.shape[2]
+    cache, new = (batch, capacity, hkv, dim), (batch, hkv, dim)
+    _check_args(q, ((k_cache, "k_cache", cache, q.dtype), (v_cache, "v_cache", cache, q.dtype),
+                    (cache_lens, "cache_lens", (batch,), torch.int32), (q, "q", q.shape, q.dtype),
+                    (k, "k", new, q.dtype), (v, "v", new, q.dtype), (out, "out", q.shape, q.dtype),
+                    (workspace, "workspace", workspace.shape if workspace is not None else (), None)))
+    code = _dtype_code(q)
+    if out is None:
+        out = torch.empty_like(q)
+    if workspace is None:
+        need = int(lib().ssd_attn_decode_workspace_bytes(batch, capacity, hq, hkv, dim, code))
+        workspace = torch.empty(max(need, 16), device=q.device, dtype=torch.uint8)
+    st = lib().ssd_attn_decode_step(_ptr(k_cache), _ptr(v_cache), _ptr(cache_lens), _ptr(q), _ptr(k), _ptr(v), batch,
+                                    capacity, hq, hkv, dim, dim ** -0.5 if scale is None else scale, code, _ptr(out),
+                                    _ptr(workspace), _nbytes(workspace), _stream(stream))
+    _check(st, "ssd_attn_decode_step")
+    return out
+
+
 def ssd_device_status(stream=None) -> int:
     """Synchronise the stream and return (and clear) the device error word."""
     return int(lib().ssd_device_status(_stream(stream)))
@@ -355,7 +502,7 @@ def ssd_profile_reset():
 
 def ssd_profile_read() -> dict:
     """{kernel name: (total_ms, launches)} since the last reset (synchronises)."""
-    n = 16
+    n = 32
     names = (ctypes.c_char_p * n)()
     ms = (ctypes.c_double * n)()
     cnt = (ctypes.c_longlong * n)()

@@ -8,6 +8,7 @@
 #include <vector>
 
 #include "common.cuh"
+#include "mixers.cuh"
 #include "prefill_tc.h"
 
 namespace ssd {
@@ -68,12 +69,14 @@ ssd_status_t from_cuda(cudaError_t e) { return e == cudaSuccess ? SSD_OK : SSD_E
 
 // ---- opt-in kernel profiling: an event pair around each launch -------------------
 enum Stage { kCumsum, kStateTc, kStateSimt, kScan, kOutTc, kOutSimt, kDecode, kCopy, kDecodeLayers, kGdn,
-             kGram, kChain, kDecodeSteps, kDecodeStepsLayers, kNumStages };
+             kGram, kChain, kDecodeSteps, kDecodeStepsLayers, kLinattn, kLinattnDecode, kAttn, kAttnDecode,
+             kNumStages };
 const char* const kStageNames[kNumStages] = {"chunk_cumsum", "chunk_state_scan_tc", "chunk_state_simt",
                                               "state_scan", "chunk_output_tc", "chunk_output_simt",
                                               "decode_step", "copy_state", "decode_step_layers",
                                               "gdn_decode_step", "block_gram_tc", "chain_prefill_tc",
-                                              "decode_steps", "decode_steps_layers"};
+                                              "decode_steps", "decode_steps_layers", "linattn_prefill",
+                                              "linattn_decode_step", "attn_prefill", "attn_decode_step"};
 
 // which tensor-core prefill batched calls take (ssd_set_prefill_path)
 std::atomic<int> g_prefill_path{SSD_PREFILL_AUTO};
@@ -406,6 +409,130 @@ ssd_status_t ssd_gdn_decode_step(float* state, const void* q, const void* k, con
     return from_cuda(profiled(kGdn, s, [&] {
         return launch_gdn_decode(dtype, state, q, k, v, gate, beta, out, batch, heads_qk, heads_v, dk, dv, s);
     }));
+}
+
+namespace {
+
+// A row of `heads` x `dim` elements every `stride`: 16-byte rows that do not overlap.
+bool stride_ok(long long stride, int heads, int dim)
+{
+    return stride % 8 == 0 && stride >= (long long)heads * dim && stride < (1LL << 36);
+}
+
+ssd_status_t check_mixer(int rows, int heads_shared, int heads, int dk, int dv, ssd_dtype_t dtype)
+{
+    if (dtype != SSD_F32 && dtype != SSD_BF16) return SSD_ERR_DTYPE;
+    if (rows < 0 || heads_shared < 1 || heads < 1 || heads > 65535 || heads % heads_shared != 0) return SSD_ERR_SHAPE;
+    if (dk < 8 || dk % 8 != 0 || dv < 8 || dv % 8 != 0) return SSD_ERR_SHAPE;
+    if (dk > kMixMaxDim || dv > kMixMaxDim) return SSD_ERR_UNSUPPORTED;
+    return SSD_OK;
+}
+
+ssd_status_t check_packed(int nseq, long long heads)
+{
+    return nseq < 1 || nseq > (1 << 20) || nseq * heads > 0x7fffffffLL ? SSD_ERR_SHAPE : SSD_OK;
+}
+
+}  // namespace
+
+size_t ssd_linattn_prefill_workspace_bytes(int nseq, int total_tokens, int heads_qk, int heads_v, int dk,
+                                           int dv, ssd_dtype_t dtype)
+{
+    if (check_mixer(total_tokens, heads_qk, heads_v, dk, dv, dtype) != SSD_OK || check_packed(nseq, heads_v) != SSD_OK)
+        return 0;
+    return linattn_simt_workspace(nseq, total_tokens, heads_v, dk, dv);
+}
+
+ssd_status_t ssd_linattn_prefill(const void* q, const void* k, const void* v, long long q_stride,
+                                 long long k_stride, long long v_stride, const float* log_decay,
+                                 const float* init_states, const int* cu_seqlens, int nseq,
+                                 int total_tokens, int heads_qk, int heads_v, int dk, int dv, float scale,
+                                 ssd_dtype_t dtype, void* out, float* final_states, void* workspace,
+                                 size_t workspace_bytes, void* stream)
+{
+    ssd_status_t st = check_mixer(total_tokens, heads_qk, heads_v, dk, dv, dtype);
+    if (st == SSD_OK) st = check_packed(nseq, heads_v);
+    if (st != SSD_OK) return st;
+    if (total_tokens > 0 && (!stride_ok(q_stride, heads_qk, dk) || !stride_ok(k_stride, heads_qk, dk) ||
+                             !stride_ok(v_stride, heads_v, dv)))
+        return SSD_ERR_SHAPE;
+    if (!log_decay || !cu_seqlens || !final_states || (total_tokens > 0 && (!q || !k || !v || !out))) return SSD_ERR_NULL;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(log_decay) || !aligned16(init_states) ||
+        !aligned16(final_states) || !aligned16(out) || !aligned16(workspace) || reinterpret_cast<uintptr_t>(cu_seqlens) % 4)
+        return SSD_ERR_ALIGN;
+    if (!workspace || workspace_bytes < ssd_linattn_prefill_workspace_bytes(nseq, total_tokens, heads_qk, heads_v, dk, dv, dtype))
+        return SSD_ERR_WORKSPACE;
+    const LinattnArgs a{q, k, v, q_stride, k_stride, v_stride, log_decay, init_states, cu_seqlens, nseq, total_tokens,
+                        heads_qk, heads_v, dk, dv, scale, out, final_states};
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return from_cuda(profiled(kLinattn, s, [&] { return launch_linattn_prefill_simt(a, dtype, workspace, s); }));
+}
+
+ssd_status_t ssd_linattn_decode_step(float* state, const void* q, const void* k, const void* v,
+                                     const float* log_decay, int batch, int heads_qk, int heads_v, int dk,
+                                     int dv, float scale, ssd_dtype_t dtype, void* out, void* stream)
+{
+    ssd_status_t st = check_mixer(batch, heads_qk, heads_v, dk, dv, dtype);
+    if (st != SSD_OK) return st;
+    if ((long long)batch * heads_v > 0x7fffffffLL) return SSD_ERR_SHAPE;
+    if (batch == 0) return SSD_OK;
+    if (!state || !q || !k || !v || !log_decay || !out) return SSD_ERR_NULL;
+    if (!aligned16(state) || !aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(log_decay) || !aligned16(out))
+        return SSD_ERR_ALIGN;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return from_cuda(profiled(kLinattnDecode, s, [&] {
+        return launch_linattn_decode(dtype, state, q, k, v, log_decay, out, batch, heads_qk, heads_v, dk, dv, scale, s);
+    }));
+}
+
+ssd_status_t ssd_attn_prefill(const void* q, const void* k, const void* v, long long q_stride,
+                              long long k_stride, long long v_stride, const int* cu_seqlens, int nseq,
+                              int total_tokens, int heads_q, int heads_kv, int headdim, float scale,
+                              ssd_dtype_t dtype, void* out, void* stream)
+{
+    ssd_status_t st = check_mixer(total_tokens, heads_kv, heads_q, headdim, headdim, dtype);
+    if (st == SSD_OK) st = check_packed(nseq, heads_q);
+    if (st != SSD_OK) return st;
+    if (total_tokens == 0) return SSD_OK;
+    if (!stride_ok(q_stride, heads_q, headdim) || !stride_ok(k_stride, heads_kv, headdim) ||
+        !stride_ok(v_stride, heads_kv, headdim))
+        return SSD_ERR_SHAPE;
+    if (!q || !k || !v || !cu_seqlens || !out) return SSD_ERR_NULL;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || reinterpret_cast<uintptr_t>(cu_seqlens) % 4)
+        return SSD_ERR_ALIGN;
+    const AttnArgs a{q, k, v, q_stride, k_stride, v_stride, cu_seqlens, nseq, total_tokens, heads_q, heads_kv, headdim,
+                     scale, out};
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return from_cuda(profiled(kAttn, s, [&] { return launch_attn_prefill_simt(a, dtype, s); }));
+}
+
+size_t ssd_attn_decode_workspace_bytes(int batch, int capacity, int heads_q, int heads_kv, int headdim,
+                                       ssd_dtype_t dtype)
+{
+    if (check_mixer(batch, heads_kv, heads_q, headdim, headdim, dtype) != SSD_OK || capacity < 1 ||
+        (long long)batch * heads_q > 0x7fffffffLL)
+        return 0;
+    return attn_decode_workspace(batch, capacity, heads_q, heads_kv, headdim);
+}
+
+ssd_status_t ssd_attn_decode_step(void* k_cache, void* v_cache, const int* cache_lens, const void* q,
+                                  const void* k, const void* v, int batch, int capacity, int heads_q,
+                                  int heads_kv, int headdim, float scale, ssd_dtype_t dtype, void* out,
+                                  void* workspace, size_t workspace_bytes, void* stream)
+{
+    ssd_status_t st = check_mixer(batch, heads_kv, heads_q, headdim, headdim, dtype);
+    if (st != SSD_OK) return st;
+    if (capacity < 1 || (long long)batch * heads_q > 0x7fffffffLL) return SSD_ERR_SHAPE;
+    if (batch == 0) return SSD_OK;
+    if (!k_cache || !v_cache || !cache_lens || !q || !k || !v || !out) return SSD_ERR_NULL;
+    if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(q) || !aligned16(k) || !aligned16(v) ||
+        !aligned16(out) || !aligned16(workspace) || reinterpret_cast<uintptr_t>(cache_lens) % 4)
+        return SSD_ERR_ALIGN;
+    if (!workspace || workspace_bytes < attn_decode_workspace(batch, capacity, heads_q, heads_kv, headdim))
+        return SSD_ERR_WORKSPACE;
+    const AttnDecodeArgs a{k_cache, v_cache, cache_lens, q, k, v, batch, capacity, heads_q, heads_kv, headdim, scale, out};
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return from_cuda(profiled(kAttnDecode, s, [&] { return launch_attn_decode(a, dtype, workspace, s); }));
 }
 
 ssd_status_t ssd_decode_step_layers(const ssd_decode_layer_t* layers, int n_layers, int batch,

@@ -1,0 +1,103 @@
+// Shared internals of the attention-like token mixers: linear attention with a decay per
+// head and causal softmax attention, over packed sequences and for single tokens.
+#pragma once
+
+#include "common.cuh"
+
+namespace ssd {
+
+// Largest head dimension of the mixers' queries, keys and values.
+constexpr int kMixMaxDim = 128;
+
+// Packed linear attention (ssd_linattn_prefill); strides are elements between tokens.
+struct LinattnArgs {
+    const void *q, *k, *v;
+    long long q_stride, k_stride, v_stride;
+    const float* log_decay;       // [heads_v]
+    const float* init_states;     // [nseq][heads_v][dk][dv] or null (zeros)
+    const int* cu;                // device [nseq + 1]
+    int nseq, total, hq, hv, dk, dv;
+    float scale;
+    void* out;                    // [total][heads_v][dv]
+    float* final_states;          // [nseq][heads_v][dk][dv]
+};
+
+// Packed causal attention (ssd_attn_prefill); strides are elements between tokens.
+struct AttnArgs {
+    const void *q, *k, *v;
+    long long q_stride, k_stride, v_stride;
+    const int* cu;                // device [nseq + 1]
+    int nseq, total, hq, hkv, dim;
+    float scale;
+    void* out;                    // [total][heads_q][dim]
+};
+
+// One token per sequence against a cache (ssd_attn_decode_step).
+struct AttnDecodeArgs {
+    void *k_cache, *v_cache;      // [batch][capacity][heads_kv][dim]
+    const int* lens;              // device [batch]
+    const void *q, *k, *v;        // [batch][heads][dim]
+    int batch, capacity, hq, hkv, dim;
+    float scale;
+    void* out;                    // [batch][heads_q][dim]
+};
+
+// ---- blocks of packed sequences ----------------------------------------------------
+// The rows of sequence s are cut into blocks of Q tokens.  Numbering block j of sequence s
+// as cu[s] / Q + s + j needs no table: ceil(len / Q) <= cu[s+1] / Q - cu[s] / Q + 1, so the
+// ranges of successive sequences do not overlap, every sequence (an empty one too) owns at
+// least one number, and there are at most total / Q + nseq of them.
+__host__ __device__ inline int packed_blocks(int total, int nseq, int Q) { return total / Q + nseq; }
+
+// Sequence, block within it, first token and sequence length of block number i.  False (and
+// SSD_ERR_SHAPE in the error word) when the offsets around it are not a valid partition; a
+// true return may still name a block past its sequence's end (j * Q >= len).
+__device__ __forceinline__ bool packed_block(const int* __restrict__ cu, int nseq, int total, int Q, int i,
+                                             int* err, int* seq, int* j, int* first, int* len)
+{
+    int lo = 0, hi = nseq - 1;                       // largest s with cu[s] / Q + s <= i
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (cu[mid] / Q + mid <= i) lo = mid; else hi = mid - 1;
+    }
+    const int a = cu[lo], b = cu[lo + 1];
+    if (a < 0 || b < a || b > total) {
+        record_error(err, SSD_ERR_SHAPE);
+        return false;
+    }
+    *seq = lo;
+    *j = i - (a / Q + lo);
+    *first = a;
+    *len = b - a;
+    return *j >= 0;
+}
+
+// Every offset, checked once by the threads of one CTA: cu[0] = 0, non-decreasing, at most
+// total.  Blocks check the two offsets that they use themselves (packed_block).
+__device__ __forceinline__ void check_offsets(const int* __restrict__ cu, int nseq, int total, int* err)
+{
+    bool bad = false;
+    for (int s = threadIdx.x; s < nseq; s += blockDim.x)
+        bad |= cu[s + 1] < cu[s] || cu[s + 1] > total || (s == 0 && cu[0] != 0);
+    if (bad) record_error(err, SSD_ERR_SHAPE);
+}
+
+// g^n for g = exp(log_decay): 1 at n = 0 whatever the decay (-inf forgets everything else).
+__device__ __forceinline__ float decay_pow(float log_decay, int n)
+{
+    return n == 0 ? 1.f : expf(log_decay * (float)n);
+}
+
+// ---- launchers -----------------------------------------------------------------------
+cudaError_t launch_linattn_decode(ssd_dtype_t dtype, float* state, const void* q, const void* k, const void* v,
+                                  const float* log_decay, void* out, int batch, int hq, int hv, int dk, int dv,
+                                  float scale, cudaStream_t s);
+size_t linattn_simt_workspace(int nseq, int total, int hv, int dk, int dv);
+cudaError_t launch_linattn_prefill_simt(const LinattnArgs& a, ssd_dtype_t dtype, void* workspace, cudaStream_t s);
+
+cudaError_t launch_attn_prefill_simt(const AttnArgs& a, ssd_dtype_t dtype, cudaStream_t s);
+
+size_t attn_decode_workspace(int batch, int capacity, int hq, int hkv, int dim);
+cudaError_t launch_attn_decode(const AttnDecodeArgs& a, ssd_dtype_t dtype, void* workspace, cudaStream_t s);
+
+}  // namespace ssd

@@ -1,0 +1,230 @@
+"""GPU parity of linear attention with a decay per head (packed prefill and single-token step)
+against the fp64 recurrence; tolerances from the kernels' roundings (mixers_ref)."""
+import pytest
+import torch
+
+import mixers_ref as ref
+import state_space_model_05_b200 as ssd
+
+pytestmark = pytest.mark.gpu
+
+bf, f32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(autouse=True, scope="module")
+def _built():
+    from state_space_model_05_b200.build import build
+    build()
+
+
+def problem(lens, hq, hv, dk, dv, dtype, seed=0, init=False):
+    n = sum(lens)
+    q, k = ref.randn(n, hq, dk, seed=seed, dtype=dtype), ref.randn(n, hq, dk, seed=seed + 1, dtype=dtype)
+    v = ref.randn(n, hv, dv, seed=seed + 2, dtype=dtype)
+    ld = -torch.exp(-6 * torch.rand(hv, generator=torch.Generator().manual_seed(seed + 3))).cuda()
+    s0 = ref.randn(len(lens), hv, dk, dv, seed=seed + 4) if init else None
+    return q, k, v, ld, s0
+
+
+def check(lens, q, k, v, ld, s0, scale, what, **kw):
+    out, fin = ssd.ssd_linattn_prefill(q, k, v, ld, ref.cu(lens), scale=scale, init_states=s0, **kw)
+    torch.cuda.synchronize()
+    assert ssd.ssd_device_status() == 0
+    wo, wf, to, tf = ref.linattn(q, k, v, ld, lens, scale, s0)
+    ref.assert_within(out[:sum(lens)], wo, to, f"{what}: out")
+    ref.assert_within(fin, wf, tf, f"{what}: final states")
+    return out, fin
+
+
+@pytest.mark.parametrize("dtype", [bf, f32])
+@pytest.mark.parametrize("hq,hv,dk,dv", [(1, 1, 8, 8), (2, 4, 64, 64), (2, 2, 128, 128), (1, 3, 72, 40), (2, 4, 128, 64),
+                                         (1, 2, 64, 128), (3, 3, 16, 120)])
+def test_shapes(dtype, hq, hv, dk, dv):
+    lens = [0, 1, 130, 17, 0, 256, 63]
+    q, k, v, ld, s0 = problem(lens, hq, hv, dk, dv, dtype, seed=dk + dv, init=True)
+    check(lens, q, k, v, ld, s0, dk ** -0.5, f"{hq}/{hv} heads, {dk} x {dv}")
+
+
+@pytest.mark.parametrize("dtype", [bf, f32])
+@pytest.mark.parametrize("n", [1, 2, 7, 8, 31, 32, 33, 63, 64, 65, 127, 128, 129, 192, 255, 256, 257, 640, 1000])
+def test_lengths(dtype, n):
+    q, k, v, ld, s0 = problem([n], 1, 2, 64 if n % 2 else 128, 128 if n % 3 else 64, dtype, seed=n)
+    check([n], q, k, v, ld, s0, 0.125, f"{n} tokens")
+
+
+@pytest.mark.parametrize("dtype", [bf, f32])
+def test_long_prompt_with_neighbours(dtype):
+    """Long enough that the tensor-core path splits it, between short sequences."""
+    lens = [3, 5003, 129]
+    q, k, v, ld, s0 = problem(lens, 1, 2, 128, 128, dtype, seed=5, init=True)
+    check(lens, q, k, v, ld, s0, 0.1, "long prompt")
+
+
+@pytest.mark.parametrize("dtype", [bf, f32])
+def test_one_long_prompt_without_state(dtype):
+    q, k, v, ld, s0 = problem([2999], 2, 2, 64, 128, dtype, seed=6)
+    check([2999], q, k, v, ld, s0, 0.1, "one long prompt")
+
+
+@pytest.mark.parametrize("dtype", [bf, f32])
+def test_decays(dtype):
+    """No decay, almost none, decays that underflow within a block, one that forgets everything, growth."""
+    lens = [300, 41]
+    q, k, v, _, s0 = problem(lens, 1, 6, 64, 64, dtype, seed=7, init=True)
+    ld = torch.tensor([0.0, -1e-7, -3.0, -200.0, float("-inf"), 0.01], device="cuda")
+    check(lens, q, k, v, ld, s0, 0.125, "decays")
+
+
+@pytest.mark.parametrize("dtype", [bf, f32])
+def test_many_short_sequences(dtype):
+    lens = [(7 * i) % 5 for i in range(300)]
+    q, k, v, ld, s0 = problem(lens, 1, 2, 64, 64, dtype, seed=8, init=True)
+    check(lens, q, k, v, ld, s0, 1.0, "short sequences")
+
+
+@pytest.mark.parametrize("dtype", [bf, f32])
+def test_slices_of_a_fused_projection_and_rows_behind(dtype):
+    """Strided q, k, v; rows past the last sequence are neither read into results nor written."""
+    lens, hq, hv, dk, dv = [70, 200], 2, 4, 64, 64
+    n, pad = sum(lens), 9
+    width = (2 * hq * dk + hv * dv) + 8
+    fused = ref.randn(n + pad, width, seed=9, dtype=dtype)
+    fused[n:] = float("nan")
+    q = fused[:, :hq * dk].unflatten(1, (hq, dk))
+    k = fused[:, hq * dk:2 * hq * dk].unflatten(1, (hq, dk))
+    v = fused[:, 2 * hq * dk:2 * hq * dk + hv * dv].unflatten(1, (hv, dv))
+    ld = -torch.rand(hv, generator=torch.Generator().manual_seed(1)).cuda() * 0.1
+    out = torch.full((n + pad, hv, dv), 7.0, dtype=dtype, device="cuda")
+    ssd.ssd_linattn_prefill(q, k, v, ld, ref.cu(lens), scale=0.2, out=out)
+    assert ssd.ssd_device_status() == 0
+    assert bool((out[n:] == 7.0).all())
+    wo, _, to, _ = ref.linattn(q[:n], k[:n], v[:n], ld, lens, 0.2)
+    ref.assert_within(out[:n], wo, to, "strided")
+
+
+@pytest.mark.parametrize("dtype", [bf, f32])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_bad_sequence_stays_its_own(dtype, bad):
+    lens = [40, 100, 200]
+    q, k, v, ld, s0 = problem(lens, 1, 2, 64, 64, dtype, seed=10, init=True)
+    for x in (q, k, v):
+        x[40:140] = bad
+    out, fin = ssd.ssd_linattn_prefill(q, k, v, ld, ref.cu(lens), init_states=s0)
+    assert ssd.ssd_device_status() == 0
+    for i, rows in ((0, slice(0, 40)), (2, slice(140, 340))):
+        wo, wf, to, tf = ref.linattn(q[rows], k[rows], v[rows], ld, [lens[i]], 1.0, s0[i:i + 1])
+        ref.assert_within(out[rows], wo, to, f"sequence {i}")
+        ref.assert_within(fin[i:i + 1], wf, tf, f"state {i}")
+    assert not torch.isfinite(out[40:140]).any()
+
+
+@pytest.mark.parametrize("dtype", [bf, f32])
+def test_later_tokens_do_not_reach_back(dtype):
+    """Tokens from t on hold NaN and infinities: the outputs before t are what they were."""
+    q, k, v, ld, s0 = problem([300], 1, 2, 64, 64, dtype, seed=11)
+    want, _ = ssd.ssd_linattn_prefill(q, k, v, ld, ref.cu([300]))
+    for t in (1, 77, 129, 290):
+        k2, v2 = k.clone(), v.clone()
+        k2[t:], v2[t:] = float("nan"), float("inf")
+        got, _ = ssd.ssd_linattn_prefill(q, k2, v2, ld, ref.cu([300]))
+        assert torch.isfinite(got[:t]).all(), t
+        wo, _, to, _ = ref.linattn(q[:t], k[:t], v[:t], ld, [t], 1.0)
+        ref.assert_within(got[:t], wo, to, f"before token {t}")
+        assert not torch.isfinite(got[t:]).any()
+
+
+def test_state_buffer_may_be_reused():
+    lens = [150, 0, 30]
+    q, k, v, ld, s0 = problem(lens, 1, 2, 64, 128, bf, seed=12, init=True)
+    out, fin = ssd.ssd_linattn_prefill(q, k, v, ld, ref.cu(lens), init_states=s0)
+    buf = s0.clone()
+    out2, fin2 = ssd.ssd_linattn_prefill(q, k, v, ld, ref.cu(lens), init_states=buf, final_states=buf)
+    assert fin2 is buf and torch.equal(out, out2) and torch.equal(fin, fin2)
+
+
+def test_no_tokens_copies_the_states():
+    z = lambda *s: torch.zeros(s, device="cuda", dtype=bf)
+    s0 = ref.randn(2, 2, 64, 64, seed=13)
+    out, fin = ssd.ssd_linattn_prefill(z(0, 1, 64), z(0, 1, 64), z(0, 2, 64), torch.zeros(2, device="cuda"),
+                                       ref.cu([0, 0]), init_states=s0)
+    assert out.shape == (0, 2, 64) and torch.equal(fin, s0)
+    _, fin = ssd.ssd_linattn_prefill(z(0, 1, 64), z(0, 1, 64), z(0, 2, 64), torch.zeros(2, device="cuda"),
+                                     ref.cu([0, 0]))
+    assert not fin.any()
+
+
+@pytest.mark.parametrize("dtype", [bf, f32])
+@pytest.mark.parametrize("offsets", [[0, 50, 40, 100], [0, 50, 101], [-4, 50, 100], [5, 50, 100]])
+def test_bad_offsets_are_reported(dtype, offsets):
+    q, k, v, ld, _ = problem([100], 1, 2, 64, 64, dtype, seed=14)
+    cu = torch.tensor(offsets, dtype=torch.int32, device="cuda")
+    ssd.ssd_linattn_prefill(q, k, v, ld, cu)
+    assert ssd.ssd_device_status() == 2                      # SSD_ERR_SHAPE
+    assert ssd.ssd_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", [bf, f32])
+def test_graph_and_side_stream_match(dtype):
+    lens = [900, 3, 260]
+    q, k, v, ld, s0 = problem(lens, 2, 4, 128, 64, dtype, seed=15, init=True)
+    cu = ref.cu(lens)
+    out, fin = ssd.ssd_linattn_prefill(q, k, v, ld, cu, init_states=s0)
+    torch.cuda.synchronize()
+    ws = torch.empty(ssd.binding.lib().ssd_linattn_prefill_workspace_bytes(3, sum(lens), 2, 4, 128, 64,
+                                                                          0 if dtype == f32 else 1), dtype=torch.uint8,
+                     device="cuda")
+    o2, f2 = torch.empty_like(out), torch.empty_like(fin)
+    stream = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        ssd.ssd_linattn_prefill(q, k, v, ld, cu, init_states=s0, out=o2, final_states=f2, workspace=ws)
+    for _ in range(2):
+        o2.zero_(), f2.zero_()
+        ws.fill_(255)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, o2) and torch.equal(fin, f2)
+    with torch.cuda.stream(stream):
+        o3, f3 = ssd.ssd_linattn_prefill(q, k, v, ld, cu, init_states=s0)
+    torch.cuda.synchronize()
+    assert torch.equal(out, o3) and torch.equal(fin, f3)
+
+
+@pytest.mark.parametrize("dtype", [bf, f32])
+@pytest.mark.parametrize("batch,hq,hv,dk,dv", [(1, 16, 32, 128, 128), (3, 2, 4, 64, 128), (5, 1, 3, 72, 40),
+                                               (64, 4, 4, 128, 64), (2, 1, 1, 8, 8), (70, 3, 9, 64, 64)])
+def test_decode_steps(dtype, batch, hq, hv, dk, dv):
+    state = ref.randn(batch, hv, dk, dv, seed=dk)
+    ld = -torch.exp(-6 * torch.rand(hv, generator=torch.Generator().manual_seed(hv))).cuda()
+    for t in range(3):
+        q, k = (ref.randn(batch, hq, dk, seed=10 * t + i, dtype=dtype) for i in (1, 2))
+        v = ref.randn(batch, hv, dv, seed=10 * t + 3, dtype=dtype)
+        wo, ws, to, ts = ref.linattn_step(state, q, k, v, ld, 0.3)
+        out = ssd.ssd_linattn_decode_step(state, q, k, v, ld, scale=0.3)
+        ref.assert_within(out, wo, to, f"step {t}: out")
+        ref.assert_within(state, ws, ts, f"step {t}: state")
+    assert ssd.ssd_device_status() == 0
+
+
+def test_decode_limits():
+    """No memory at all, none lost, and an empty batch."""
+    state = ref.randn(1, 2, 64, 64, seed=3)
+    old = state.clone()
+    q, k, v = ref.randn(1, 1, 64, seed=4), ref.randn(1, 1, 64, seed=5), ref.randn(1, 2, 64, seed=6)
+    ssd.ssd_linattn_decode_step(state, q, k, v, torch.tensor([float("-inf"), 0.0], device="cuda"))
+    kv = k[0, 0][:, None] * v[0, :, None, :]
+    assert torch.equal(state[0, 0], kv[0])
+    torch.testing.assert_close(state[0, 1], old[0, 1] + kv[1], rtol=2 ** -22, atol=2 ** -22)
+    e = lambda *s: torch.empty(s, device="cuda")
+    assert ssd.ssd_linattn_decode_step(e(0, 2, 64, 64), e(0, 1, 64), e(0, 1, 64), e(0, 2, 64), e(2)).shape == (0, 2, 64)
+
+
+@pytest.mark.parametrize("dtype", [bf, f32])
+def test_prefill_then_steps_is_prefill(dtype):
+    """The state after T tokens and k steps is the state after T + k tokens."""
+    q, k, v, ld, s0 = problem([205], 2, 4, 64, 128, dtype, seed=16, init=True)
+    out, state = ssd.ssd_linattn_prefill(q[:200], k[:200], v[:200], ld, ref.cu([200]), scale=0.1, init_states=s0)
+    outs = [ssd.ssd_linattn_decode_step(state, q[t:t + 1], k[t:t + 1], v[t:t + 1], ld, scale=0.1) for t in range(200, 205)]
+    wo, wf, to, tf = ref.linattn(q, k, v, ld, [205], 0.1, s0)
+    ref.assert_within(torch.cat([out, *outs]), wo, to, "outputs")
+    ref.assert_within(state, wf, tf, "state")
