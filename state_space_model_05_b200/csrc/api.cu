@@ -503,7 +503,9 @@ ssd_status_t ssd_attn_prefill(const void* q, const void* k, const void* v, long 
     const AttnArgs a{q, k, v, q_stride, k_stride, v_stride, cu_seqlens, nseq, total_tokens, heads_q, heads_kv, headdim,
                      scale, out};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return from_cuda(profiled(kAttn, s, [&] { return launch_attn_prefill_simt(a, dtype, s); }));
+    return from_cuda(profiled(kAttn, s, [&] {
+        return dtype == SSD_BF16 && attn_tc_supported(a) ? launch_attn_prefill_tc(a, s) : launch_attn_prefill_simt(a, dtype, s);
+    }));
 }
 
 size_t ssd_attn_decode_workspace_bytes(int batch, int capacity, int heads_q, int heads_kv, int headdim,

@@ -1,0 +1,415 @@
+// Causal softmax attention over packed prompts on the tensor cores (bf16, sm_100a):
+// tcgen05.mma with scores, probabilities and outputs in TMEM, operands staged by TMA.
+//
+//     o_t = sum_{s<=t} p_s v_s / sum_{s<=t} p_s,   p_s = 2^(c q_t.k_s - m),   c = scale log2(e)
+//
+// One CTA takes 256 query rows of one key/value head, as two tiles of 128 rows.  A row is a
+// (token, query head of the group) pair, so the heads that share a key/value head share its
+// loads and a tile spans 128 / group tokens, which also keeps the masked part of the last key
+// tile small.  Keys are visited 128 at a time.  Per key tile i and query tile j:
+//     S = Q_j K_i^T  (TMEM)  ->  softmax warps: row maximum, P = 2^(c S - m) as bf16 over S
+//     O_j += P V_i   (TMEM, A operand from TMEM)
+// Roles: four softmax warps per query tile (one thread per row), one issuing warp per query
+// tile, one TMA warp and one warp that looks after the values of the masked key tiles.  While
+// one tile's softmax runs, the tensor cores work for the other tile.
+//
+// The running maximum moves only when a row's scores exceed it by 2^8: until then p stays
+// below 2^8 and nothing has to be rescaled; the sum and O use the same m, so the quotient is
+// exact.  A move rescales O in TMEM by its own warp, which is safe because S_i is issued
+// only after P V_(i-1) has completed.  P is rounded to bf16 (the operand type; its sum is
+// taken before the rounding, in fp32), as is the output; everything else is fp32.
+#include <cuda.h>
+
+#include "mixers.cuh"
+#include "prefill_tc.h"
+#include "ptx.cuh"
+
+namespace ssd {
+
+using namespace ptx;
+
+namespace {
+
+constexpr int kRows = 128;                                 // query rows per tile
+constexpr int kKeys = 128;                                 // keys per tile
+constexpr int kHalf = kKeys * 128;                         // one 64-dimension half of a tile, 128-byte rows
+constexpr int kThreads = 384;                              // 8 softmax warps, TMA, 2 MMA, values
+constexpr int kWarpTma = 8, kWarpMma = 9, kWarpValues = 11;
+constexpr int kMaxMasked = 3;                              // key tiles that hold a diagonal of the CTA
+constexpr float kLog2e = 1.44269504088896341f;
+constexpr float kSlack = 8.f;                              // log2 of the largest p before the maximum moves
+
+template <int D>
+struct Cfg {
+    static constexpr int kHalves = D / 64;
+    static constexpr int kTile = kHalves * kHalf;          // bytes of a Q, K or V tile
+    static constexpr int kSlots = D == 128 ? 5 : 8;        // K and V tiles in flight
+    static constexpr int kKv = 2 * kTile;
+    static constexpr int kBar = kKv + kSlots * kTile;
+    static constexpr int kNumBars = 1 + 2 * kSlots + 6 + 2 * kMaxMasked;
+    static constexpr int kTm = kBar + kNumBars * 8;
+    static constexpr int kBytes = kTm + 16 + 1024;
+    // TMEM columns: two score tiles, two outputs
+    static constexpr uint32_t kS = 0, kO = 256;
+    static_assert(kBytes <= 227 * 1024, "shared memory");
+};
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+        "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+        "add.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
+// Zeroes value rows from `rows` on (another sequence's) and looks for values that are not
+// finite among the others: 0 x inf would carry them into rows that must not see them.  Those
+// are zeroed too and reported, and the epilogue adds them where they belong.
+template <int D>
+__device__ bool fix_values(uint8_t* sv, int rows, int lane)
+{
+    constexpr int kChunks = D / 8;                         // 16-byte chunks per row
+    uint32_t bad = 0;
+    const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
+    __nv_bfloat162 acc = zero;
+    for (int i = lane; i < kKeys * kChunks; i += 32) {
+        const int r = (i / 8) % kKeys;                     // halves of [128 rows][8 chunks]
+        uint4* p = reinterpret_cast<uint4*>(sv) + i;       // (the swizzle permutes chunks within a row)
+        if (r >= rows) {
+            *p = make_uint4(0u, 0u, 0u, 0u);
+        } else {
+            const uint4 u = *p;
+            const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&u);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc = __hfma2(h[j], zero, acc);
+        }
+    }
+    bad = __hisnan(acc.x) || __hisnan(acc.y);
+    const bool any = __any_sync(0xffffffffu, bad);
+    if (any) {
+        for (int i = lane; i < kKeys * kChunks; i += 32) {
+            uint4* p = reinterpret_cast<uint4*>(sv) + i;
+            uint4 u = *p;
+            uint32_t* w = reinterpret_cast<uint32_t*>(&u);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if ((w[j] & 0x7F80u) == 0x7F80u) w[j] &= 0xFFFF0000u;
+                if ((w[j] & 0x7F800000u) == 0x7F800000u) w[j] &= 0xFFFFu;
+            }
+            *p = u;
+        }
+    }
+    return any;
+}
+
+struct AttnMaps { CUtensorMap q, k, v; };
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+attn_prefill_tc_kernel(const __grid_constant__ AttnMaps maps, const AttnArgs a, int* err)
+{
+    using L = Cfg<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::kBar);
+    uint64_t *q_full = bars, *full = bars + 1, *empty = full + L::kSlots, *s_full = empty + L::kSlots,
+             *p_full = s_full + 2, *pv_done = p_full + 2, *v_in = pv_done + 2, *v_ok = v_in + kMaxMasked;
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + L::kTm);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L::kTm + 4);
+    int* bad_tiles = reinterpret_cast<int*>(sm + L::kTm + 8);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    // this CTA's rows: blocks with the most keys first, the key/value heads side by side
+    const int group = a.hq / a.hkv, span = kRows / group;  // tokens per query tile
+    const int hk = blockIdx.x % a.hkv, blk = gridDim.x / a.hkv - 1 - blockIdx.x / a.hkv;
+    if (blockIdx.x == 0) check_offsets(a.cu, a.nseq, a.total, err);
+    int seq, j0, first, len;
+    if (!packed_block(a.cu, a.nseq, a.total, 2 * span, blk, err, &seq, &j0, &first, &len)) return;
+    const int t0 = j0 * 2 * span;                          // first token, within the sequence
+    if (t0 >= len) return;
+    // key tiles that each query tile needs; from `masked` on a tile reaches past some row's diagonal
+    const int nk0 = (min(t0 + span, len) - 1) / kKeys + 1;
+    const int nk1 = t0 + span < len ? (min(t0 + 2 * span, len) - 1) / kKeys + 1 : 0;
+    const int nk = max(nk0, nk1), masked = (t0 + 1) / kKeys;
+
+    if (tid == 0) {
+        mbar_init(q_full, 1);
+        for (int s = 0; s < L::kSlots; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 2);
+        }
+        for (int j = 0; j < 2; ++j) {
+            mbar_init(&s_full[j], 1);
+            mbar_init(&p_full[j], kRows);
+            mbar_init(&pv_done[j], 1);
+        }
+        for (int i = 0; i < kMaxMasked; ++i) {
+            mbar_init(&v_in[i], 1);
+            mbar_init(&v_ok[i], 1);
+        }
+        *abort_flag = 0;
+        *bad_tiles = 0;
+        fence_mbar_init();
+    }
+    if (warp == kWarpMma) {
+        tmem_alloc(tslot, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tslot;
+    auto kv = [&](int n) { return sm + L::kKv + (n % L::kSlots) * L::kTile; };   // K_i is tile 2 i, V_i tile 2 i + 1
+    auto wait = [&](uint64_t* bar, int phase) { return mbar_wait_or_abort(bar, phase & 1, err, abort_flag); };
+
+    if (warp == kWarpTma) {
+        if (lane == 0) {
+            const int tiles = nk1 > 0 ? 2 : 1;
+            mbar_expect_tx(q_full, tiles * L::kHalves * 128 * group * span);
+            for (int j = 0; j < tiles; ++j)
+                for (int h = 0; h < L::kHalves; ++h)
+                    tma_load_3d(sm + j * L::kTile + h * kHalf, &maps.q, 64 * h, hk * group, first + t0 + j * span, q_full);
+            for (int n = 0; n < 2 * nk; ++n) {
+                const int s = n % L::kSlots;
+                if (n >= L::kSlots && !wait(&empty[s], n / L::kSlots - 1)) break;
+                // a masked tile's values go to the values warp first: its barriers are used once,
+                // so that it need not follow the slots' phases (`full` then only marks the turn)
+                const bool to_fix = (n & 1) && (n >> 1) >= masked;
+                uint64_t* bar = to_fix ? &v_in[(n >> 1) - masked] : &full[s];
+                mbar_expect_tx(bar, L::kTile);
+                for (int h = 0; h < L::kHalves; ++h)
+                    tma_load_3d(kv(n) + h * kHalf, n & 1 ? &maps.v : &maps.k, 64 * h, hk, first + (n >> 1) * kKeys, bar);
+                if (to_fix) mbar_arrive(&full[s]);
+            }
+        }
+    } else if (warp == kWarpMma || warp == kWarpMma + 1) {
+        if (lane == 0) {
+            const int j = warp - kWarpMma, n_own = j ? nk1 : nk0;
+            const uint32_t tS = tmem + L::kS + j * 128, tO = tmem + L::kO + j * 128;
+            constexpr uint32_t idS = idesc_bf16_f32(128, kKeys, false, false);
+            constexpr uint32_t idO = idesc_bf16_f32(128, D, false, true);
+            const uint64_t dQ = smem_desc_sw128(smem_u32(sm + j * L::kTile), 16, 1024);
+            bool ok = n_own == 0 || wait(q_full, 0);
+            for (int i = 0; i < nk && ok; ++i) {
+                const int nK = 2 * i, nV = 2 * i + 1, sK = nK % L::kSlots, sV = nV % L::kSlots;
+                ok = wait(&full[sK], nK / L::kSlots);
+                if (!ok) break;
+                if (i >= n_own) {                          // a tile that only the other query tile needs
+                    mbar_arrive(&empty[sK]);
+                    ok = wait(&full[sV], nV / L::kSlots);
+                    mbar_arrive(&empty[sV]);
+                    continue;
+                }
+                // S over P: the product that reads P has to be complete
+                ok = i == 0 || wait(&pv_done[j], i - 1);
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t dK = smem_desc_sw128(smem_u32(kv(nK)), 16, 1024);
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks) {
+                    const uint32_t off = (ks >> 2) * kHalf + (ks & 3) * 32;
+                    umma_f16(tS, desc_advance(dQ, off), desc_advance(dK, off), idS, ks > 0 ? 1u : 0u);
+                }
+                umma_commit(&empty[sK]);
+                umma_commit(&s_full[j]);
+                ok = wait(&full[sV], nV / L::kSlots) && (i < masked || wait(&v_ok[i - masked], 0)) && wait(&p_full[j], i);
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t dV = smem_desc_sw128(smem_u32(kv(nV)), kHalf, 1024);
+#pragma unroll
+                for (int ks = 0; ks < kKeys / 16; ++ks)
+                    umma_f16_ts(tO, tS + ks * 8, desc_advance(dV, ks * 2048), idO, (i > 0 || ks > 0) ? 1u : 0u);
+                umma_commit(&empty[sV]);
+                umma_commit(&pv_done[j]);
+            }
+            // no TMEM is released with products in flight
+            if (ok && n_own > 0) wait(&pv_done[j], n_own - 1);
+        }
+    } else if (warp == kWarpValues) {
+        for (int i = masked; i < nk; ++i) {
+            if (!wait(&v_in[i - masked], 0)) break;
+            const bool bad = fix_values<D>(kv(2 * i + 1), min(kKeys, len - i * kKeys), lane);
+            if (bad && lane == 0) atomicOr(bad_tiles, 1 << (i - masked));
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&v_ok[i - masked]);
+        }
+    } else {
+        // ---------------------------------------------------------------- softmax
+        const int j = warp >> 2, r = tid & 127;            // query tile, row
+        const int tok = r / group, t = t0 + j * span + tok;   // the row's token, within the sequence
+        const bool live = tok < span && t < len;
+        const int n_own = j ? nk1 : nk0;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t tS = tmem + lanes + L::kS + j * 128, tO = tmem + lanes + L::kO + j * 128;
+        const float c = a.scale * kLog2e;
+        const bool positive = c > 0.f;
+        const float mul = positive ? c : 1.f;              // else the scores are scaled before the maximum
+        float m = __int_as_float(0xff800000), l = 0.f;
+        bool ok = true;
+        for (int i = 0; i < n_own; ++i) {
+            ok = __all_sync(0xffffffffu, wait(&s_full[j], i));
+            if (!ok) break;
+            tc_fence_after();
+            uint32_t s[128];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) tmem_ld32(tS + 32 * q, reinterpret_cast<uint32_t(&)[32]>(s[32 * q]));
+            tmem_wait_ld();
+            float* x = reinterpret_cast<float*>(s);
+            if (!positive) {
+#pragma unroll
+                for (int e = 0; e < 128; ++e) x[e] *= c;
+            }
+            if (i >= masked) {
+                const int limit = t - i * kKeys;           // keys past the row's own token
+#pragma unroll
+                for (int e = 0; e < 128; ++e) x[e] = e <= limit ? x[e] : __int_as_float(0xff800000);
+            }
+            float top[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+            for (int e = 4; e < 128; e += 8) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) top[q] = e + q + 4 < 128 ? max3(top[q], x[e + q], x[e + q + 4]) : fmaxf(top[q], x[e + q]);
+            }
+            const float now = fmaxf(max3(top[0], top[1], top[2]), top[3]) * mul;
+            float keep = 1.f;
+            if (now > m + kSlack) {
+                keep = ex2(m - now);                       // 0 from the initial -inf
+                m = now;
+                l *= keep;
+            }
+            if (i > 0 && __any_sync(0xffffffffu, keep != 1.f)) {
+#pragma unroll
+                for (int q = 0; q < D / 32; ++q) {
+                    uint32_t o[32];
+                    tmem_ld32(tO + 32 * q, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
+                    tmem_st16(tO + 32 * q, reinterpret_cast<uint32_t(&)[16]>(o[0]));
+                    tmem_st16(tO + 32 * q + 16, reinterpret_cast<uint32_t(&)[16]>(o[16]));
+                }
+            }
+            const float base = m == __int_as_float(0xff800000) ? 0.f : m;   // a row of -inf so far keeps p = 0
+            const float2 mul2 = make_float2(mul, mul), base2 = make_float2(-base, -base);
+            float2 sum[2] = {make_float2(l, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                uint32_t p[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    float2 y = ffma2(make_float2(x[32 * q + 2 * e], x[32 * q + 2 * e + 1]), mul2, base2);
+                    y.x = ex2(y.x);
+                    y.y = ex2(y.y);
+                    sum[e & 1] = add2(sum[e & 1], y);
+                    p[e] = pack_bf16x2(y.x, y.y);
+                }
+                tmem_st16(tS + 16 * q, p);
+            }
+            const float2 both = add2(sum[0], sum[1]);
+            l = both.x + both.y;
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(&p_full[j]);
+        }
+        if (ok && n_own > 0 && __all_sync(0xffffffffu, wait(&pv_done[j], n_own - 1))) {
+            tc_fence_after();
+            const float inv = 1.f / l;
+            const int bad = *bad_tiles;
+            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) +
+                                 ((size_t)(first + t) * a.hq + (size_t)hk * group + (r - tok * group)) * a.dim;
+#pragma unroll
+            for (int q = 0; q < D / 32; ++q) {
+                uint32_t o[32];
+                tmem_ld32(tO + 32 * q, o);
+                tmem_wait_ld();
+                if (!live) continue;
+                float y[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) y[e] = __uint_as_float(o[e]) * inv;
+                if (bad) {
+                    // values that are not finite, taken out of the product: p > 0 times one of
+                    // them is that value, whatever p is
+                    for (int i = masked; i < nk; ++i) {
+                        if (!(bad >> (i - masked) & 1)) continue;
+                        for (int s0 = i * kKeys; s0 <= min(t, i * kKeys + kKeys - 1); ++s0) {
+                            const __nv_bfloat16* vr = static_cast<const __nv_bfloat16*>(a.v) +
+                                                      (size_t)(first + s0) * a.v_stride + (size_t)hk * a.dim;
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) {
+                                if (32 * q + e < a.dim) {
+                                    const float z = __bfloat162float(vr[32 * q + e]);
+                                    if (!(fabsf(z) < __int_as_float(0x7f800000))) y[e] += z;
+                                }
+                            }
+                        }
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 32; e += 8)
+                    if (32 * q + e < a.dim)
+                        *reinterpret_cast<uint4*>(out + 32 * q + e) =
+                            make_uint4(pack_bf16x2(y[e], y[e + 1]), pack_bf16x2(y[e + 2], y[e + 3]),
+                                       pack_bf16x2(y[e + 4], y[e + 5]), pack_bf16x2(y[e + 6], y[e + 7]));
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kWarpMma) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// [tokens][heads][dim] bf16 with `stride` elements between tokens, read in boxes of 64
+// dimensions x `heads_box` heads x `tokens_box` tokens; what lies outside reads as zero.
+bool token_map(CUtensorMap* m, const void* p, int dim, int heads, int tokens, long long stride, int heads_box, int tokens_box)
+{
+    const uint64_t dims[3] = {(uint64_t)dim, (uint64_t)heads, (uint64_t)tokens};
+    const uint64_t strides[2] = {(uint64_t)dim * 2, (uint64_t)stride * 2};
+    const uint32_t box[3] = {64, (uint32_t)heads_box, (uint32_t)tokens_box};
+    return tc_encode_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, p, dims, strides, box, true);
+}
+
+template <int D>
+cudaError_t launch_t(const AttnArgs& a, cudaStream_t s)
+{
+    const int group = a.hq / a.hkv, span = kRows / group;
+    AttnMaps maps;
+    if (!token_map(&maps.q, a.q, a.dim, a.hq, a.total, a.q_stride, group, span) ||
+        !token_map(&maps.k, a.k, a.dim, a.hkv, a.total, a.k_stride, 1, kKeys) ||
+        !token_map(&maps.v, a.v, a.dim, a.hkv, a.total, a.v_stride, 1, kKeys))
+        return cudaErrorInvalidValue;
+    cudaError_t e = cudaFuncSetAttribute(attn_prefill_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kBytes);
+    if (e != cudaSuccess) return e;
+    const long long grid = (long long)packed_blocks(a.total, a.nseq, 2 * span) * a.hkv;
+    if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
+    attn_prefill_tc_kernel<D><<<(unsigned)grid, kThreads, Cfg<D>::kBytes, s>>>(maps, a, device_error_word());
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+bool attn_tc_supported(const AttnArgs& a) { return a.hq / a.hkv <= kRows; }
+
+cudaError_t launch_attn_prefill_tc(const AttnArgs& a, cudaStream_t s)
+{
+    return a.dim <= 64 ? launch_t<64>(a, s) : launch_t<128>(a, s);
+}
+
+}  // namespace ssd

@@ -95,6 +95,9 @@ cudaError_t launch_linattn_decode(ssd_dtype_t dtype, float* state, const void* q
 size_t linattn_simt_workspace(int nseq, int total, int hv, int dk, int dv);
 cudaError_t launch_linattn_prefill_simt(const LinattnArgs& a, ssd_dtype_t dtype, void* workspace, cudaStream_t s);
 
+// Tensor-core attention (bf16), for up to 128 query heads per key/value head.
+bool attn_tc_supported(const AttnArgs& a);
+cudaError_t launch_attn_prefill_tc(const AttnArgs& a, cudaStream_t s);
 cudaError_t launch_attn_prefill_simt(const AttnArgs& a, ssd_dtype_t dtype, cudaStream_t s);
 
 size_t attn_decode_workspace(int batch, int capacity, int hq, int hkv, int dim);
