@@ -440,7 +440,9 @@ size_t ssd_linattn_prefill_workspace_bytes(int nseq, int total_tokens, int heads
 {
     if (check_mixer(total_tokens, heads_qk, heads_v, dk, dv, dtype) != SSD_OK || check_packed(nseq, heads_v) != SSD_OK)
         return 0;
-    return linattn_simt_workspace(nseq, total_tokens, heads_v, dk, dv);
+    const size_t need = dtype == SSD_BF16 ? linattn_tc_workspace(nseq, total_tokens, heads_v, dk, dv)
+                                          : linattn_simt_workspace(nseq, total_tokens, heads_v, dk, dv);
+    return need > kAlign ? need : kAlign;
 }
 
 ssd_status_t ssd_linattn_prefill(const void* q, const void* k, const void* v, long long q_stride,
@@ -465,7 +467,9 @@ ssd_status_t ssd_linattn_prefill(const void* q, const void* k, const void* v, lo
     const LinattnArgs a{q, k, v, q_stride, k_stride, v_stride, log_decay, init_states, cu_seqlens, nseq, total_tokens,
                         heads_qk, heads_v, dk, dv, scale, out, final_states};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return from_cuda(profiled(kLinattn, s, [&] { return launch_linattn_prefill_simt(a, dtype, workspace, s); }));
+    return from_cuda(profiled(kLinattn, s, [&] {
+        return dtype == SSD_BF16 ? launch_linattn_prefill_tc(a, workspace, s) : launch_linattn_prefill_simt(a, workspace, s);
+    }));
 }
 
 ssd_status_t ssd_linattn_decode_step(float* state, const void* q, const void* k, const void* v,

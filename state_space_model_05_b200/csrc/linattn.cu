@@ -1,5 +1,5 @@
 // Linear attention with a decay per head on the CUDA cores: the single-token step on the
-// state, and the chunked prefill in fp32 arithmetic (any storage type).
+// state, and the chunked prefill of fp32 tensors (bf16: linattn_tc.cu).
 //
 //     S_t = g S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t,   g = exp(log_decay[h])
 //
@@ -319,10 +319,9 @@ size_t linattn_simt_workspace(int nseq, int total, int hv, int dk, int dv)
     return (size_t)packed_blocks(total, nseq, kTok) * hv * dk * dv * sizeof(float);
 }
 
-cudaError_t launch_linattn_prefill_simt(const LinattnArgs& a, ssd_dtype_t dtype, void* workspace, cudaStream_t s)
+cudaError_t launch_linattn_prefill_simt(const LinattnArgs& a, void* workspace, cudaStream_t s)
 {
-    float* states = static_cast<float*>(workspace);
-    return dtype == SSD_F32 ? prefill_t<float>(a, states, s) : prefill_t<__nv_bfloat16>(a, states, s);
+    return prefill_t<float>(a, static_cast<float*>(workspace), s);
 }
 
 }  // namespace ssd

@@ -1,0 +1,759 @@
+// Linear attention with a decay per head over packed prompts on the tensor cores (bf16,
+// sm_100a): tcgen05.mma with accumulators in TMEM, operands staged by TMA.
+//
+//     S_t = g S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t,   g = exp(log_decay[h])
+//
+// in blocks of n <= 128 tokens with the carried state S (dk x dv) at the block's start:
+//     o_t = scale (sum_{s<=t} g^(t-s) (q_t.k_s) v_s + g^(t+1) S^T q_t)
+//     S  <- g^n S + sum_s (g^(n-1-s) k_s) v_s^T
+// The decay does not depend on the tokens, so every factor comes from one table g^0 .. g^128.
+//
+// linattn_output_kernel: one CTA walks the blocks of one (segment, value head), the state in
+// the state warps' registers (fp32).  A segment is a sequence, or `blocks` blocks of a long
+// one; linattn_segment_kernel, launched before it when a sequence can be that long, forms
+// every segment's own state from zero, and the walk starts from
+// S = g^L (.. (g^L S_0 + U_0) ..) + U_(j-1).  Splitting costs a second read of k and v and
+// buys segments for all SMs; the host picks the length (segment_blocks).
+//
+// Per block: S = Q K^T, masked and decayed into P (bf16, over S in TMEM), Yd = P V; Yo = Q S from
+// the state's bf16 image; U = K~^T V with K~ = g^(n-1-s) k_s.  K~ is carried as the sum of three
+// bf16 numbers (24 bits), so that the state keeps fp32 accuracy; P and the state's image are
+// rounded to bf16 once, each by at most half the output's own rounding step.  The four
+// products take less time than the block's loads, so their number does not show.
+#include <cuda.h>
+
+#include "mixers.cuh"
+#include "prefill_tc.h"
+#include "ptx.cuh"
+
+namespace ssd {
+
+using namespace ptx;
+
+namespace {
+
+constexpr int kBlk = 128;                                  // tokens per block
+constexpr int kHalf = kBlk * 128;                          // 64 dimensions of a block's rows
+constexpr int kPiece = 32;                                 // tokens of K~ formed at a time
+constexpr int kPieces = kBlk / kPiece;
+
+// Bytes of a 32-token piece of K~: three parts, each [dk / 64][32 rows][128 bytes].
+template <int DK> constexpr int kPartBytes = DK / 64 * kPiece * 128;
+
+// g^0 .. g^128 and, reversed, g^31 .. g^0
+struct Powers { float up[kBlk + 4]; float down[kPiece]; };
+
+__device__ __forceinline__ void fill_powers(Powers* p, float ld, int tid, int threads)
+{
+    for (int i = tid; i <= kBlk; i += threads) p->up[i] = decay_pow(ld, i);
+    for (int i = tid; i < kPiece; i += threads) p->down[i] = decay_pow(ld, kPiece - 1 - i);
+}
+
+// One 16-byte chunk (eight keys' elements of one token) times w, as three bf16 parts.
+__device__ __forceinline__ void split3(const uint4& k, float w, uint4 (&part)[3])
+{
+    const uint32_t in[4] = {k.x, k.y, k.z, k.w};
+    uint32_t out[3][4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        float a = bf16lo(in[j]) * w, b = bf16hi(in[j]) * w;
+#pragma unroll
+        for (int q = 0; q < 3; ++q) {
+            out[q][j] = pack_bf16x2(a, b);
+            a -= bf16lo(out[q][j]);
+            b -= bf16hi(out[q][j]);
+        }
+    }
+#pragma unroll
+    for (int q = 0; q < 3; ++q) part[q] = make_uint4(out[q][0], out[q][1], out[q][2], out[q][3]);
+}
+
+// A thread's chunks of piece p of a block's keys, weighted and split; the swizzle permutes
+// chunks within a row by the row's number mod 8, which the piece keeps.
+template <int DK, int kThreads>
+struct Convert {
+    static constexpr int kChunks = DK / 8 * kPiece / kThreads;
+    uint4 part[kChunks][3];
+    // w[s]: the weight of token s of the piece; rows from n on are zero whatever they hold
+    __device__ __forceinline__ void form(const uint8_t* keys, int p, int n, const float* up, float extra, int tid)
+    {
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+            const int i = tid + c * kThreads, half = i / (kPiece * 8), r = (i >> 3) % kPiece, s = p * kPiece + r;
+            const uint4 k = *reinterpret_cast<const uint4*>(keys + half * kHalf + p * kPiece * 128 + (i % (kPiece * 8)) * 16);
+            if (s < n) {
+                split3(k, up[n - 1 - s] * extra, part[c]);
+            } else {
+#pragma unroll
+                for (int q = 0; q < 3; ++q) part[c][q] = make_uint4(0u, 0u, 0u, 0u);
+            }
+        }
+    }
+    __device__ __forceinline__ void write(uint8_t* dst, int tid) const
+    {
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+            const int i = tid + c * kThreads;
+#pragma unroll
+            for (int q = 0; q < 3; ++q) *reinterpret_cast<uint4*>(dst + q * kPartBytes<DK> + i * 16) = part[c][q];
+        }
+    }
+};
+
+// The products of one piece: U (+)= K~^T V over its 32 tokens.
+template <int DK, int DV>
+__device__ __forceinline__ void issue_state(uint32_t tU, uint32_t conv, uint32_t values, int p, bool fresh)
+{
+    constexpr uint32_t id = idesc_bf16_f32(128, DV, true, true);
+    const uint64_t dV = smem_desc_sw128(values + p * kPiece * 128, kHalf, 1024);
+#pragma unroll
+    for (int q = 0; q < 3; ++q) {
+        // dk = 64: rows 64 .. 127 of the product are never read
+        const uint64_t dK = smem_desc_sw128(conv + q * kPartBytes<DK>, kPiece * 128, 1024);
+#pragma unroll
+        for (int ks = 0; ks < kPiece / 16; ++ks)
+            umma_f16(tU, desc_advance(dK, ks * 2048), desc_advance(dV, ks * 2048), id, (fresh && q == 0 && ks == 0) ? 0u : 1u);
+    }
+}
+
+struct LinattnMaps { CUtensorMap q, k, v; };
+
+// The segment of this CTA: sequence, segment within it, its first token and number of tokens.
+struct Segment { int seq, j, first, start, len, seq_len; };
+
+__device__ __forceinline__ bool this_segment(const LinattnArgs& a, int blocks, int* err, Segment* s)
+{
+    int first, len;
+    if (!packed_block(a.cu, a.nseq, a.total, blocks * kBlk, blockIdx.x / a.hv, err, &s->seq, &s->j, &first, &len)) return false;
+    s->start = s->j * blocks * kBlk;
+    if (s->j > 0 && s->start >= len) return false;
+    s->seq_len = len;
+    s->len = min(blocks * kBlk, len - s->start);
+    s->first = first + s->start;
+    return true;
+}
+
+// ================================================================ a segment's own state
+constexpr int kSegThreads = 384, kSegConv = 256, kSegStages = 2, kSegSlots = 2;
+
+template <int DK, int DV>
+struct SegCfg {
+    static constexpr int kKeys = DK / 64 * kHalf, kValues = DV / 64 * kHalf;
+    static constexpr int kStage = kKeys + kValues;
+    static constexpr int kConv = kSegStages * kStage;
+    static constexpr int kPow = kConv + kSegSlots * 3 * kPartBytes<DK> + 4096;   // (rows past dk = 64 are read)
+    static constexpr int kBar = (kPow + (int)sizeof(Powers) + 7) / 8 * 8;
+    static constexpr int kTm = kBar + (2 * kSegStages + 2 * kSegSlots + 1) * 8;
+    static constexpr int kBytes = kTm + 16 + 1024;
+    static_assert(kBytes <= 227 * 1024, "shared memory");
+};
+
+template <int DK, int DV>
+__global__ void __launch_bounds__(kSegThreads, 1)
+linattn_segment_kernel(const __grid_constant__ LinattnMaps maps, const LinattnArgs a, int blocks,
+                       float4* __restrict__ states, int* err)
+{
+    using L = SegCfg<DK, DV>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::kBar);
+    uint64_t *full = bars, *empty = full + kSegStages, *conv_full = empty + kSegStages, *conv_empty = conv_full + kSegSlots,
+             *done = conv_empty + kSegSlots;
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + L::kTm);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L::kTm + 4);
+    Powers* pw = reinterpret_cast<Powers*>(sm + L::kPow);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int h = blockIdx.x % a.hv;
+    griddep_launch_dependents();
+    Segment sg;
+    // the last segment of a sequence hands its state to no one
+    if (!this_segment(a, blocks, err, &sg) || sg.start + blocks * kBlk >= sg.seq_len) return;
+
+    if (tid == 0) {
+        for (int s = 0; s < kSegStages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int s = 0; s < kSegSlots; ++s) {
+            mbar_init(&conv_full[s], kSegConv);
+            mbar_init(&conv_empty[s], 1);
+        }
+        mbar_init(done, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    const float ld = a.log_decay[h];
+    fill_powers(pw, ld, tid, kSegThreads);
+    if (warp == 1) {
+        tmem_alloc(tslot, 128);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tslot;
+    auto wait = [&](uint64_t* bar, int phase) { return mbar_wait_or_abort(bar, phase & 1, err, abort_flag); };
+    auto conv = [&](int n) { return sm + L::kConv + (n % kSegSlots) * 3 * kPartBytes<DK>; };
+
+    if (warp == 0) {
+        if (lane == 0) {
+            const int hq = h / (a.hv / a.hq);
+            for (int c = 0; c < blocks; ++c) {
+                const int s = c % kSegStages;
+                if (c >= kSegStages && !wait(&empty[s], c / kSegStages - 1)) break;
+                uint8_t* st = sm + s * L::kStage;
+                mbar_expect_tx(&full[s], L::kStage);
+                for (int x = 0; x < DK; x += 64) tma_load_3d(st + x / 64 * kHalf, &maps.k, x, hq, sg.first + c * kBlk, &full[s]);
+                for (int x = 0; x < DV; x += 64)
+                    tma_load_3d(st + L::kKeys + x / 64 * kHalf, &maps.v, x, h, sg.first + c * kBlk, &full[s]);
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            bool ok = true;
+            for (int n = 0; n < blocks * kPieces && ok; ++n) {
+                const int c = n / kPieces, p = n % kPieces;
+                ok = wait(&conv_full[n % kSegSlots], n / kSegSlots);
+                if (!ok) break;
+                tc_fence_after();
+                issue_state<DK, DV>(tmem, smem_u32(conv(n)), smem_u32(sm + (c % kSegStages) * L::kStage + L::kKeys), p, n == 0);
+                umma_commit(&conv_empty[n % kSegSlots]);
+                if (p == kPieces - 1) umma_commit(&empty[c % kSegStages]);
+            }
+            umma_commit(done);
+            wait(done, 0);                                 // no TMEM is released with products in flight
+        }
+    } else if (warp >= 4) {
+        const int ctid = tid - 128;
+        bool ok = true;
+        for (int c = 0; c < blocks && ok; ++c) {
+            ok = wait(&full[c % kSegStages], c / kSegStages);
+            // weights from the segment's end: the products accumulate over all its blocks
+            const float extra = decay_pow(ld, (blocks - 1 - c) * kBlk);
+            for (int p = 0; p < kPieces && ok; ++p) {
+                const int n = c * kPieces + p;
+                Convert<DK, kSegConv> x;
+                x.form(sm + (c % kSegStages) * L::kStage, p, kBlk, pw->up, extra, ctid);
+                ok = n < kSegSlots || wait(&conv_empty[n % kSegSlots], n / kSegSlots - 1);
+                if (!ok) break;
+                x.write(conv(n), ctid);
+                fence_proxy_async_smem();
+                mbar_arrive(&conv_full[n % kSegSlots]);
+            }
+        }
+        if (__all_sync(0xffffffffu, ok && wait(done, 0))) {
+            tc_fence_after();
+            // quads of columns as [column quad][row]: consecutive lanes write consecutive quads
+            const int row = (warp & 3) * 32 + lane, c0 = ((warp - 4) >> 2) * (DV / 2);
+            float4* dst = states + (size_t)blockIdx.x * (DK * DV / 4);
+#pragma unroll
+            for (int q = 0; q < DV / 32; ++q) {
+                uint32_t v[16];
+                tmem_ld16(tmem + ((uint32_t)((warp & 3) * 32) << 16) + c0 + 16 * q, v);
+                tmem_wait_ld();
+                if (row < DK) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        dst[(c0 / 4 + 4 * q + e) * DK + row] =
+                            make_float4(__uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1]),
+                                        __uint_as_float(v[4 * e + 2]), __uint_as_float(v[4 * e + 3]));
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 128);
+    }
+}
+
+// ================================================================ outputs and final states
+constexpr int kOutThreads = 640;                           // TMA, 3 MMA, 4 conversion, 8 state, 4 output warps
+constexpr int kConvThreads = 128;
+constexpr int kWarpConv = 4, kWarpState = 8, kWarpOut = 16;
+
+template <int DK, int DV>
+struct OutCfg {
+    static constexpr int kKeys = DK / 64 * kHalf, kValues = DV / 64 * kHalf;
+    static constexpr int kImage = DV / 64 * DK * 128;      // state as [dv / 64][dk rows][128 bytes]
+    static constexpr int kQSlots = DK + DV <= 192 ? 2 : 1;
+    static constexpr int kK = kQSlots * kKeys, kV = kK + 2 * kKeys, kImg = kV + 2 * kValues;
+    static constexpr int kConv = kImg + kImage;
+    static constexpr int kPow = kConv + 3 * kPartBytes<DK> + (DK == 64 ? 4096 : 0);
+    static constexpr int kBar = (kPow + (int)sizeof(Powers) + 7) / 8 * 8;
+    static constexpr int kTm = kBar + 32 * 8;
+    static constexpr int kBytes = kTm + 32 + 1024;
+    static_assert(kBytes <= 227 * 1024, "shared memory");
+    // TMEM columns: scores (then P), the block's part, the carried part, the block's state
+    static constexpr uint32_t kS = 0, kYd = 128, kYo = 256, kU = 384;
+};
+
+template <int DK, int DV>
+__global__ void __launch_bounds__(kOutThreads, 1)
+linattn_output_kernel(const __grid_constant__ LinattnMaps maps, const LinattnArgs a, int blocks,
+                      const float4* __restrict__ states, int* err)
+{
+    using L = OutCfg<DK, DV>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::kBar);
+    uint64_t *q_full = bars, *q_empty = bars + 2, *k_full = bars + 4, *k_empty = bars + 6, *v_full = bars + 8,
+             *v_empty = bars + 10, *v_ok = bars + 12, *s_full = bars + 14, *p_full = bars + 15, *yd_full = bars + 16,
+             *yd_free = bars + 17, *yo_full = bars + 18, *yo_free = bars + 19, *img_full = bars + 20, *u_full = bars + 21,
+             *u_free = bars + 22, *conv_full = bars + 23, *conv_empty = bars + 24;
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + L::kTm);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L::kTm + 4);
+    volatile int* bad_values = reinterpret_cast<volatile int*>(sm + L::kTm + 8);     // [4], by block mod 4
+    Powers* pw = reinterpret_cast<Powers*>(sm + L::kPow);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int h = blockIdx.x % a.hv;
+    if (blockIdx.x == 0) check_offsets(a.cu, a.nseq, a.total, err);
+    Segment sg;
+    if (!this_segment(a, blocks, err, &sg)) return;
+    const int nb = (sg.len + kBlk - 1) / kBlk;             // 0 for an empty sequence
+    const int last = sg.len - (nb - 1) * kBlk;             // tokens of the last block
+    const bool ends = sg.start + sg.len >= sg.seq_len;     // this segment writes the final state
+
+    if (tid == 0) {
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&q_full[s], 1);
+            mbar_init(&q_empty[s], 2);
+            mbar_init(&k_full[s], 1);
+            mbar_init(&k_empty[s], 1 + kConvThreads / 32);
+            mbar_init(&v_full[s], 1);
+            mbar_init(&v_empty[s], 2);
+            mbar_init(&v_ok[s], kConvThreads / 32);
+        }
+        mbar_init(s_full, 1);
+        mbar_init(p_full, 128);
+        mbar_init(yd_full, 1);
+        mbar_init(yd_free, 128);
+        mbar_init(yo_full, 1);
+        mbar_init(yo_free, 128);
+        mbar_init(img_full, 8);
+        mbar_init(u_full, 1);
+        mbar_init(u_free, 8);
+        mbar_init(conv_full, kConvThreads / 32);
+        mbar_init(conv_empty, 1);
+        *abort_flag = 0;
+        for (int i = 0; i < 4; ++i) bad_values[i] = 0;
+        fence_mbar_init();
+    }
+    const float ld = a.log_decay[h];
+    fill_powers(pw, ld, tid, kOutThreads);
+    if (warp == 1) {
+        tmem_alloc(tslot, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tslot;
+    auto wait = [&](uint64_t* bar, int phase) { return mbar_wait_or_abort(bar, phase & 1, err, abort_flag); };
+    auto wait_warp = [&](uint64_t* bar, int phase) { return (bool)__all_sync(0xffffffffu, wait(bar, phase)); };
+    auto qslot = [&](int c) { return sm + (c % L::kQSlots) * L::kKeys; };
+    auto kslot = [&](int c) { return sm + L::kK + (c & 1) * L::kKeys; };
+    auto vslot = [&](int c) { return sm + L::kV + (c & 1) * L::kValues; };
+    auto tokens = [&](int c) { return c == nb - 1 ? last : kBlk; };
+    constexpr int QS = L::kQSlots;
+
+    if (warp == 0) {
+        // ---------------------------------------------------------------- loads
+        if (lane == 0) {
+            const int hq = h / (a.hv / a.hq);
+            // two streams, polled: a block's keys and values, and its queries, whose slot is free
+            // earlier or later than theirs
+            int kv = 0, cq = 0;
+            uint32_t idle = 0;
+            while (kv < nb || cq < nb) {
+                bool moved = false;
+                if (kv < nb && (kv < 2 || (mbar_test_wait(&k_empty[kv & 1], (kv / 2 - 1) & 1) &&
+                                           mbar_test_wait(&v_empty[kv & 1], (kv / 2 - 1) & 1)))) {
+                    const int row = sg.first + kv * kBlk, s = kv & 1;
+                    mbar_expect_tx(&k_full[s], L::kKeys);
+                    for (int x = 0; x < DK; x += 64) tma_load_3d(kslot(kv) + x / 64 * kHalf, &maps.k, x, hq, row, &k_full[s]);
+                    mbar_expect_tx(&v_full[s], L::kValues);
+                    for (int x = 0; x < DV; x += 64) tma_load_3d(vslot(kv) + x / 64 * kHalf, &maps.v, x, h, row, &v_full[s]);
+                    if (kv > cq)                           // queries that wait for their slot wait in the L2
+                        for (int x = 0; x < DK; x += 64) tma_prefetch_3d(&maps.q, x, hq, row);
+                    ++kv;
+                    moved = true;
+                }
+                if (cq < nb && (cq < QS || mbar_test_wait(&q_empty[cq % QS], (cq / QS - 1) & 1))) {
+                    mbar_expect_tx(&q_full[cq % QS], L::kKeys);
+                    for (int x = 0; x < DK; x += 64)
+                        tma_load_3d(qslot(cq) + x / 64 * kHalf, &maps.q, x, hq, sg.first + cq * kBlk, &q_full[cq % QS]);
+                    ++cq;
+                    moved = true;
+                }
+                if (moved) {
+                    idle = 0;
+                } else if (++idle >= (1u << 24)) {
+                    record_error(err, SSD_ERR_TIMEOUT);
+                    *abort_flag = 1;
+                    break;
+                } else if ((idle & 1023u) == 0 && *abort_flag) {
+                    break;
+                }
+            }
+        }
+    } else if (warp == 1) {
+        // ---------------------------------------------------------------- S = Q K^T, Yd = P V
+        if (lane == 0) {
+            constexpr uint32_t idS = idesc_bf16_f32(128, kBlk, false, false), idY = idesc_bf16_f32(128, DV, false, true);
+            bool ok = true;
+            for (int c = 0; c < nb && ok; ++c) {
+                ok = wait(&q_full[c % QS], c / QS) && wait(&k_full[c & 1], c / 2) && (c == 0 || wait(yd_full, c - 1));
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t dQ = smem_desc_sw128(smem_u32(qslot(c)), 16, 1024), dK = smem_desc_sw128(smem_u32(kslot(c)), 16, 1024);
+#pragma unroll
+                for (int ks = 0; ks < DK / 16; ++ks) {
+                    const uint32_t off = (ks >> 2) * kHalf + (ks & 3) * 32;
+                    umma_f16(tmem + L::kS, desc_advance(dQ, off), desc_advance(dK, off), idS, ks > 0 ? 1u : 0u);
+                }
+                umma_commit(&k_empty[c & 1]);
+                umma_commit(&q_empty[c % QS]);
+                umma_commit(s_full);
+                ok = wait(&v_ok[c & 1], c / 2) && wait(p_full, c) && (c == 0 || wait(yd_free, c - 1));
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t dV = smem_desc_sw128(smem_u32(vslot(c)), kHalf, 1024);
+#pragma unroll
+                for (int ks = 0; ks < kBlk / 16; ++ks)
+                    umma_f16_ts(tmem + L::kYd, tmem + L::kS + ks * 8, desc_advance(dV, ks * 2048), idY, ks > 0 ? 1u : 0u);
+                umma_commit(&v_empty[c & 1]);
+                umma_commit(yd_full);
+            }
+            if (ok && nb > 0) wait(yd_full, nb - 1);       // no TMEM is released with products in flight
+        }
+    } else if (warp == 2) {
+        // ---------------------------------------------------------------- Yo = Q S
+        if (lane == 0) {
+            constexpr uint32_t id = idesc_bf16_f32(128, DV, false, true);
+            bool ok = true;
+            for (int c = 0; c < nb && ok; ++c) {
+                ok = wait(&q_full[c % QS], c / QS) && wait(img_full, c) && (c == 0 || wait(yo_free, c - 1));
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t dQ = smem_desc_sw128(smem_u32(qslot(c)), 16, 1024);
+                const uint64_t dS = smem_desc_sw128(smem_u32(sm + L::kImg), DK * 128, 1024);
+#pragma unroll
+                for (int ks = 0; ks < DK / 16; ++ks)
+                    umma_f16(tmem + L::kYo, desc_advance(dQ, (ks >> 2) * kHalf + (ks & 3) * 32), desc_advance(dS, ks * 2048), id,
+                             ks > 0 ? 1u : 0u);
+                umma_commit(&q_empty[c % QS]);
+                umma_commit(yo_full);
+            }
+            if (ok && nb > 0) wait(yo_full, nb - 1);
+        }
+    } else if (warp == 3) {
+        // ---------------------------------------------------------------- U = K~^T V
+        if (lane == 0) {
+            bool ok = true;
+            int n = 0;
+            for (int c = 0; c < nb && ok; ++c) {
+                const int pieces = (tokens(c) + kPiece - 1) / kPiece;
+                for (int p = 0; p < pieces; ++p, ++n) {
+                    ok = wait(conv_full, n) && (p > 0 || c == 0 || wait(u_free, c - 1));
+                    if (!ok) break;
+                    tc_fence_after();
+                    issue_state<DK, DV>(tmem + L::kU, smem_u32(sm + L::kConv), smem_u32(vslot(c)), p, p == 0);
+                    umma_commit(conv_empty);
+                }
+                if (!ok) break;
+                umma_commit(&v_empty[c & 1]);
+                umma_commit(u_full);
+            }
+            if (ok && nb > 0) wait(u_full, nb - 1);
+        }
+    } else if (warp < kWarpState) {
+        // ---------------------------------------------------------------- values checked, K~ formed
+        const int ctid = tid - kWarpConv * 32;
+        const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
+        bool ok = true;
+        int n = 0;
+        for (int c = 0; c < nb && ok; ++c) {
+            const int rows = tokens(c);
+            ok = wait_warp(&v_full[c & 1], c / 2);
+            if (!ok) break;
+            // rows behind the sequence's end are another's: zeroed, since 0 x inf is not 0.  Values
+            // that are not finite are left to the output warps, as P's zeros would not hide them.
+            __nv_bfloat162 acc = zero;
+#pragma unroll 4
+            for (int i = ctid; i < kBlk * DV / 8; i += kConvThreads) {
+                uint4* p = reinterpret_cast<uint4*>(vslot(c)) + i;
+                if ((i >> 3) % kBlk >= rows) {
+                    *p = make_uint4(0u, 0u, 0u, 0u);
+                } else {
+                    const uint4 u = *p;
+                    const __nv_bfloat162* x = reinterpret_cast<const __nv_bfloat162*>(&u);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc = __hfma2(x[e], zero, acc);
+                }
+            }
+            if (__hisnan(acc.x) || __hisnan(acc.y)) bad_values[c & 3] = c + 1;
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&v_ok[c & 1]);
+            ok = wait_warp(&k_full[c & 1], c / 2);
+            for (int p = 0; p < (rows + kPiece - 1) / kPiece && ok; ++p, ++n) {
+                Convert<DK, kConvThreads> x;
+                x.form(kslot(c), p, rows, pw->up, 1.f, ctid);
+                ok = n == 0 || wait_warp(conv_empty, n - 1);
+                if (!ok) break;
+                x.write(sm + L::kConv, ctid);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(conv_full);
+            }
+            if (lane == 0) mbar_arrive(&k_empty[c & 1]);
+        }
+    } else if (warp < kWarpOut) {
+        // ---------------------------------------------------------------- the carried state
+        constexpr int NC = DV / 2;                         // columns per thread
+        const int quarter = warp & 3, row = quarter * 32 + lane, c0 = ((warp - kWarpState) >> 2) * NC;
+        const bool mine = row < a.dk;
+        float S[NC];
+        const size_t at = (((size_t)sg.seq * a.hv + h) * a.dk + row) * a.dv + c0;
+#pragma unroll
+        for (int e = 0; e < NC; e += 4) {
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (a.init_states && mine && c0 + e < a.dv) x = *reinterpret_cast<const float4*>(a.init_states + at + e);
+            S[e] = x.x; S[e + 1] = x.y; S[e + 2] = x.z; S[e + 3] = x.w;
+        }
+        if (sg.j > 0) {
+            griddep_wait();                                // the segments' states come from the kernel before
+            const float g = decay_pow(ld, blocks * kBlk);
+            const float4* src = states + (size_t)(blockIdx.x - sg.j * a.hv) * (DK * DV / 4) + (c0 / 4) * DK + row;
+            for (int i = 0; i < sg.j; ++i, src += (size_t)a.hv * (DK * DV / 4)) {
+#pragma unroll
+                for (int e = 0; e < NC; e += 4) {
+                    const float4 u = row < DK ? src[e / 4 * DK] : make_float4(0.f, 0.f, 0.f, 0.f);
+                    S[e] = fmaf(g, S[e], u.x);
+                    S[e + 1] = fmaf(g, S[e + 1], u.y);
+                    S[e + 2] = fmaf(g, S[e + 2], u.z);
+                    S[e + 3] = fmaf(g, S[e + 3], u.w);
+                }
+            }
+        }
+        // bf16 image: row `row` of each 64-column half, 16-byte chunks permuted by the row
+        auto write_image = [&]() {
+            if (row < DK) {
+#pragma unroll
+                for (int e = 0; e < NC; e += 8) {
+                    const int col = c0 + e;
+                    *reinterpret_cast<uint4*>(sm + L::kImg + (col >> 6) * (DK * 128) + row * 128 + (((col & 63) >> 3) ^ (row & 7)) * 16) =
+                        make_uint4(pack_bf16x2(S[e], S[e + 1]), pack_bf16x2(S[e + 2], S[e + 3]),
+                                   pack_bf16x2(S[e + 4], S[e + 5]), pack_bf16x2(S[e + 6], S[e + 7]));
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(img_full);
+        };
+        if (nb > 0) write_image();
+        bool ok = true;
+        for (int c = 0; c < nb; ++c) {
+            ok = wait_warp(u_full, c);
+            if (!ok) break;
+            tc_fence_after();
+            const float g = pw->up[tokens(c)];
+#pragma unroll
+            for (int q = 0; q < NC / 16; ++q) {
+                uint32_t v[16];
+                tmem_ld16(tmem + ((uint32_t)(quarter * 32) << 16) + L::kU + c0 + 16 * q, v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) S[16 * q + e] = fmaf(g, S[16 * q + e], __uint_as_float(v[e]));
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(u_free);
+            if (c + 1 < nb) {
+                ok = wait_warp(yo_full, c);                // the product that reads the image has completed
+                if (!ok) break;
+                write_image();
+            }
+        }
+        if (ok && ends && mine) {
+#pragma unroll
+            for (int e = 0; e < NC; e += 4)
+                if (c0 + e < a.dv)
+                    *reinterpret_cast<float4*>(a.final_states + at + e) = make_float4(S[e], S[e + 1], S[e + 2], S[e + 3]);
+        }
+    } else {
+        // ---------------------------------------------------------------- P, and the outputs
+        const int quarter = warp & 3, r = quarter * 32 + lane;
+        const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+        const float g_out = pw->up[r + 1];
+        for (int c = 0; c < nb; ++c) {
+            if (!wait_warp(s_full, c)) break;
+            tc_fence_after();
+#pragma unroll
+            for (int kc = 0; kc < 4; ++kc) {
+                uint32_t pk[16];
+                if (kc <= quarter) {                       // the same for the warp's 32 rows
+                    uint32_t v[32];
+                    tmem_ld32(tmem + lanes + L::kS + 32 * kc, v);
+                    tmem_wait_ld();
+                    if (kc < quarter) {
+                        // g^(t-s) = g^(t-e) g^(e-s), e the last of these 32 columns
+                        const float u = pw->up[r - 32 * kc - 31];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const float4 w = *reinterpret_cast<const float4*>(&pw->down[4 * e]);
+                            pk[2 * e] = pack_bf16x2(__uint_as_float(v[4 * e]) * (u * w.x), __uint_as_float(v[4 * e + 1]) * (u * w.y));
+                            pk[2 * e + 1] = pack_bf16x2(__uint_as_float(v[4 * e + 2]) * (u * w.z), __uint_as_float(v[4 * e + 3]) * (u * w.w));
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const float x = 2 * e <= lane ? __uint_as_float(v[2 * e]) * pw->up[lane - 2 * e] : 0.f;
+                            const float y = 2 * e + 1 <= lane ? __uint_as_float(v[2 * e + 1]) * pw->up[lane - 2 * e - 1] : 0.f;
+                            pk[e] = pack_bf16x2(x, y);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) pk[e] = 0u;
+                }
+                // P over S: this warp has read these columns, and the ones after them lie further on
+                tmem_st16(tmem + lanes + L::kS + 16 * kc, pk);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(p_full);
+            if (!wait_warp(yd_full, c) || !wait_warp(yo_full, c)) break;
+            tc_fence_after();
+            const int t = c * kBlk + r;                    // token within the segment
+            const bool live = t < sg.len;
+            const bool bad = bad_values[c & 3] == c + 1;
+            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + ((size_t)(sg.first + t) * a.hv + h) * a.dv;
+#pragma unroll
+            for (int q = 0; q < DV / 16; ++q) {
+                uint32_t yd[16], yo[16];
+                tmem_ld16(tmem + lanes + L::kYd + 16 * q, yd);
+                tmem_ld16(tmem + lanes + L::kYo + 16 * q, yo);
+                tmem_wait_ld();
+                float y[16];
+                if (bad && live) {
+                    // the block holds a value that is not finite: the row's own sum, so that only
+                    // the rows from that token on see it
+                    const size_t base = sg.first + (size_t)c * kBlk, hq = (size_t)(h / (a.hv / a.hq)) * a.dk;
+                    const __nv_bfloat16* qr = static_cast<const __nv_bfloat16*>(a.q) + (base + r) * a.q_stride + hq;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) y[e] = 0.f;
+                    for (int s = 0; s <= r; ++s) {
+                        const __nv_bfloat16* kr = static_cast<const __nv_bfloat16*>(a.k) + (base + s) * a.k_stride + hq;
+                        const __nv_bfloat16* vr = static_cast<const __nv_bfloat16*>(a.v) + (base + s) * a.v_stride + (size_t)h * a.dv;
+                        float p = 0.f;
+                        for (int d = 0; d < a.dk; ++d) p = fmaf(__bfloat162float(qr[d]), __bfloat162float(kr[d]), p);
+                        p *= pw->up[r - s];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            if (16 * q + e < a.dv) y[e] = fmaf(p, __bfloat162float(vr[16 * q + e]), y[e]);
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) y[e] = __uint_as_float(yd[e]);
+                }
+#pragma unroll
+                for (int e = 0; e < 16; ++e) y[e] = a.scale * fmaf(g_out, __uint_as_float(yo[e]), y[e]);
+                if (live) {
+#pragma unroll
+                    for (int e = 0; e < 16; e += 8)
+                        if (16 * q + e < a.dv)
+                            *reinterpret_cast<uint4*>(out + 16 * q + e) =
+                                make_uint4(pack_bf16x2(y[e], y[e + 1]), pack_bf16x2(y[e + 2], y[e + 3]),
+                                           pack_bf16x2(y[e + 4], y[e + 5]), pack_bf16x2(y[e + 6], y[e + 7]));
+                }
+            }
+            tc_fence_before();
+            mbar_arrive(yd_free);
+            mbar_arrive(yo_free);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// ---------------------------------------------------------------- host side
+// Blocks per segment: the length at which the waves of the two kernels cost least for
+// sequences of average length.  Per 128-token block the output kernel takes about 3 us and the
+// segment kernel 1.6 us when all SMs are busy, either about 4 us to start and end.
+int segment_blocks(int nseq, int total, int hv)
+{
+    const long long sms = tc_sm_count();
+    const long long avg = max(1LL, ((long long)total / nseq + kBlk - 1) / kBlk);
+    int best = 4;
+    double best_cost = 0;
+    for (int len = 4; len <= 1024; ++len) {
+        const long long segs = (avg + len - 1) / len, units = segs * nseq * hv, inner = (segs - 1) * nseq * hv;
+        const double cost = (double)((units + sms - 1) / sms) * (3.0 * min((long long)len, avg) + 4.0) +
+                            (double)((inner + sms - 1) / sms) * (1.6 * len + 4.0);
+        if (len == 4 || cost < best_cost) {
+            best = len;
+            best_cost = cost;
+        }
+        if (len >= avg) break;
+    }
+    return best;
+}
+
+bool token_map(CUtensorMap* m, const void* p, int dim, int heads, int tokens, long long stride)
+{
+    const uint64_t dims[3] = {(uint64_t)dim, (uint64_t)heads, (uint64_t)tokens};
+    const uint64_t strides[2] = {(uint64_t)dim * 2, (uint64_t)stride * 2};
+    const uint32_t box[3] = {64, 1, kBlk};
+    return tc_encode_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, p, dims, strides, box, true);
+}
+
+template <int DK, int DV>
+cudaError_t launch_t(const LinattnArgs& a, float4* states, cudaStream_t s)
+{
+    LinattnMaps maps = {};
+    if (a.total > 0 && (!token_map(&maps.q, a.q, a.dk, a.hq, a.total, a.q_stride) ||
+                        !token_map(&maps.k, a.k, a.dk, a.hq, a.total, a.k_stride) ||
+                        !token_map(&maps.v, a.v, a.dv, a.hv, a.total, a.v_stride)))
+        return cudaErrorInvalidValue;
+    const int blocks = segment_blocks(a.nseq, a.total, a.hv);
+    const long long grid = (long long)packed_blocks(a.total, a.nseq, blocks * kBlk) * a.hv;
+    if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
+    int* err = device_error_word();
+    cudaError_t e = cudaSuccess;
+    if (a.total > blocks * kBlk) {
+        e = cudaFuncSetAttribute(linattn_segment_kernel<DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 SegCfg<DK, DV>::kBytes);
+        if (e != cudaSuccess) return e;
+        linattn_segment_kernel<DK, DV><<<(unsigned)grid, kSegThreads, SegCfg<DK, DV>::kBytes, s>>>(maps, a, blocks, states, err);
+    }
+    e = cudaFuncSetAttribute(linattn_output_kernel<DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, OutCfg<DK, DV>::kBytes);
+    if (e != cudaSuccess) return e;
+    linattn_output_kernel<DK, DV><<<(unsigned)grid, kOutThreads, OutCfg<DK, DV>::kBytes, s>>>(maps, a, blocks, states, err);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t linattn_tc_workspace(int nseq, int total, int hv, int dk, int dv)
+{
+    const int blocks = segment_blocks(nseq, total, hv);
+    if (total <= blocks * kBlk) return 0;
+    return (size_t)packed_blocks(total, nseq, blocks * kBlk) * hv * (dk <= 64 ? 64 : 128) * (dv <= 64 ? 64 : 128) * sizeof(float);
+}
+
+cudaError_t launch_linattn_prefill_tc(const LinattnArgs& a, void* workspace, cudaStream_t s)
+{
+    float4* states = static_cast<float4*>(workspace);
+    if (a.dk <= 64) return a.dv <= 64 ? launch_t<64, 64>(a, states, s) : launch_t<64, 128>(a, states, s);
+    return a.dv <= 64 ? launch_t<128, 64>(a, states, s) : launch_t<128, 128>(a, states, s);
+}
+
+}  // namespace ssd

@@ -92,8 +92,11 @@ __device__ __forceinline__ float decay_pow(float log_decay, int n)
 cudaError_t launch_linattn_decode(ssd_dtype_t dtype, float* state, const void* q, const void* k, const void* v,
                                   const float* log_decay, void* out, int batch, int hq, int hv, int dk, int dv,
                                   float scale, cudaStream_t s);
+// Packed prefill: bf16 on the tensor cores, fp32 on the CUDA cores.
+size_t linattn_tc_workspace(int nseq, int total, int hv, int dk, int dv);
+cudaError_t launch_linattn_prefill_tc(const LinattnArgs& a, void* workspace, cudaStream_t s);
 size_t linattn_simt_workspace(int nseq, int total, int hv, int dk, int dv);
-cudaError_t launch_linattn_prefill_simt(const LinattnArgs& a, ssd_dtype_t dtype, void* workspace, cudaStream_t s);
+cudaError_t launch_linattn_prefill_simt(const LinattnArgs& a, void* workspace, cudaStream_t s);
 
 // Tensor-core attention (bf16), for up to 128 query heads per key/value head.
 bool attn_tc_supported(const AttnArgs& a);
