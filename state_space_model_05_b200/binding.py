@@ -107,12 +107,14 @@ def _dtype_code(t: torch.Tensor) -> int:
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream=None):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    """The cudaStream_t of ``stream``, or of the current device's current stream."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream
 
 
 def _nbytes(t: torch.Tensor) -> int:
@@ -130,7 +132,7 @@ def _need(t: torch.Tensor, name: str, dtype=None):
 
 def _rank(t: torch.Tensor, name: str, layout: str):
     """Raise unless ``t`` has one axis per name in ``layout`` (e.g. "[batch][seqlen][nheads]")."""
-    if t.dim() != layout.count("["):
+    if t.ndim != layout.count("["):
         raise ValueError(f"{name} must be {layout}, got shape {tuple(t.shape)}")
 
 
@@ -140,6 +142,15 @@ def _check_args(ref: torch.Tensor, specs):
     (tensor or None, name, expected shape, dtype or None); every tensor given must have that
     shape, live on ``ref``'s device, be a contiguous CUDA tensor and (if stated) have that
     dtype.  ``ref`` must be on the current device, whose stream the library launches on."""
+    if ref.is_cuda:                                # the usual case: nothing to report
+        device = ref.get_device()
+        for t, _, shape, dtype in specs:
+            if t is not None and (t.shape != shape or not t.is_cuda or t.get_device() != device
+                                  or (dtype is not None and t.dtype != dtype) or not t.is_contiguous()):
+                break
+        else:
+            if device == torch._C._cuda_getDevice():
+                return
     for t, name, shape, _ in specs:
         if t is not None and tuple(t.shape) != tuple(shape):
             raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
@@ -371,10 +382,12 @@ def _check_mixer(ref: torch.Tensor, strided, specs):
     """_check_args for calls some of whose tensors (``strided``: tensor, name, shape) may have
     their tokens apart."""
     for t, name, shape in strided:
-        if tuple(t.shape) != tuple(shape):
+        if t.shape != shape:
             raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     _check_args(ref, specs)
     for t, name, _ in strided:
+        if t.is_cuda and t.dtype == ref.dtype and t.get_device() == ref.get_device():
+            continue
         if not t.is_cuda:
             raise ValueError(f"{name} must be a CUDA tensor")
         if t.dtype != ref.dtype:

@@ -17,7 +17,7 @@ LIB = os.path.join(HERE, "libssd.so")
 GEN_LIB = os.path.join(HERE, "libssd_inputs.so")
 GEN_SRC = os.path.join(CSRC, "gen", "gen_inputs.cu")
 
-SOURCES = ["api.cu", "attn.cu", "attn_tc.cu", "decode.cu", "gdn_decode.cu", "linattn.cu", "linattn_tc.cu", "prefill_simt.cu", "prefill_tc.cu", "prefill_fused.cu",
+SOURCES = ["api.cu", "attn.cu", "attn_decode.cu", "attn_tc.cu", "decode.cu", "gdn_decode.cu", "linattn.cu", "linattn_tc.cu", "prefill_simt.cu", "prefill_tc.cu", "prefill_fused.cu",
            "prefill_noalloc.cu", "selftest.cu"]
 HEADERS = ["common.cuh", "mixers.cuh", "ptx.cuh", "prefill_tc.h"]
 

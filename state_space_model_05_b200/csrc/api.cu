@@ -518,7 +518,7 @@ size_t ssd_attn_decode_workspace_bytes(int batch, int capacity, int heads_q, int
     if (check_mixer(batch, heads_kv, heads_q, headdim, headdim, dtype) != SSD_OK || capacity < 1 ||
         (long long)batch * heads_q > 0x7fffffffLL)
         return 0;
-    return attn_decode_workspace(batch, capacity, heads_q, heads_kv, headdim);
+    return attn_decode_workspace(batch, capacity, heads_q, heads_kv, dtype);
 }
 
 ssd_status_t ssd_attn_decode_step(void* k_cache, void* v_cache, const int* cache_lens, const void* q,
@@ -534,7 +534,7 @@ ssd_status_t ssd_attn_decode_step(void* k_cache, void* v_cache, const int* cache
     if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(q) || !aligned16(k) || !aligned16(v) ||
         !aligned16(out) || !aligned16(workspace) || reinterpret_cast<uintptr_t>(cache_lens) % 4)
         return SSD_ERR_ALIGN;
-    if (!workspace || workspace_bytes < attn_decode_workspace(batch, capacity, heads_q, heads_kv, headdim))
+    if (!workspace || workspace_bytes < attn_decode_workspace(batch, capacity, heads_q, heads_kv, dtype))
         return SSD_ERR_WORKSPACE;
     const AttnDecodeArgs a{k_cache, v_cache, cache_lens, q, k, v, batch, capacity, heads_q, heads_kv, headdim, scale, out};
     cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -103,7 +103,7 @@ bool attn_tc_supported(const AttnArgs& a);
 cudaError_t launch_attn_prefill_tc(const AttnArgs& a, cudaStream_t s);
 cudaError_t launch_attn_prefill_simt(const AttnArgs& a, ssd_dtype_t dtype, cudaStream_t s);
 
-size_t attn_decode_workspace(int batch, int capacity, int hq, int hkv, int dim);
+size_t attn_decode_workspace(int batch, int capacity, int hq, int hkv, ssd_dtype_t dtype);
 cudaError_t launch_attn_decode(const AttnDecodeArgs& a, ssd_dtype_t dtype, void* workspace, cudaStream_t s);
 
 }  // namespace ssd
