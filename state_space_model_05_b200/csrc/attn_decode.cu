@@ -551,14 +551,19 @@ attn_decode_f32_kernel(const AttnDecodeArgs a, float* __restrict__ pieces, int* 
 }
 
 // ================================================================ cut units
-// Joins the pieces of a unit that more than one CTA worked on: one CTA per unit, one thread per
-// dimension, the pieces in the order of their CTAs.
+// Joins the pieces of a unit that more than one CTA worked on: one CTA per unit and query
+// head, one thread per dimension, the pieces in the order of their CTAs.  A long row is cut
+// into hundreds of pieces: their weights are formed side by side first, so that the sum's loads
+// do not wait for one another.
 template <typename T, int kUnitRows>
 __global__ void __launch_bounds__(kMixMaxDim)
 attn_decode_join_kernel(const AttnDecodeArgs a, const float* __restrict__ pieces, int max_ctas)
 {
+    extern __shared__ float weight[];                      // [max_ctas]
+    __shared__ float red[2][kMixMaxDim / 32];
     const Units un(a.hq, a.hkv, kUnitRows);
-    const int b = blockIdx.x / un.per_row, u = blockIdx.x - b * un.per_row, d = threadIdx.x;
+    const int b = blockIdx.x / a.hq, h = blockIdx.x - b * a.hq, d = threadIdx.x;
+    const int hk = h / un.group, r = (h - hk * un.group) % kUnitRows, u = hk * un.blocks + (h - hk * un.group) / kUnitRows;
     const Located at = locate<kMixMaxDim>(a.lens, a.batch, a.capacity, un.per_row, true, nullptr, [&](long long) { return (long long)b; });
     const int n = row_tiles(a.lens[b], a.capacity);
     griddep_wait();                                        // also where nothing is to join: this grid ends after the one before
@@ -572,23 +577,37 @@ attn_decode_join_kernel(const AttnDecodeArgs a, const float* __restrict__ pieces
     };
     const int c0 = owner(t0), c1 = owner(t1 - 1);
     if (c0 == c1) return;
-    const int hk = u / un.blocks, first = (u - hk * un.blocks) * kUnitRows;
-    const int h0 = hk * un.group + first, rows = min(kUnitRows, un.group - first);
-    for (int r = 0; r < rows; ++r) {
-        float m = neg_inf(), l = 0.f, o = 0.f;
-        for (int c = c0; c <= c1; ++c) {
-            // the piece that starts at its unit's start lies in its CTA's second slot
-            const float* p = pieces + (size_t)(2 * c + (c == c0 ? 1 : 0)) * kPiece<kUnitRows>;
-            const float pm = p[kUnitRows * kMixMaxDim + r], pl = p[kUnitRows * kMixMaxDim + kUnitRows + r];
-            const float top = fmaxf(m, pm), base = top == neg_inf() ? 0.f : top;
-            const float keep = exp2f(m - base), add = exp2f(pm - base);
-            const float po = d < a.dim ? p[r * kMixMaxDim + d] : 0.f;
-            o = o * keep + po * add;
-            l = l * keep + pl * add;
-            m = top;
-        }
-        if (d < a.dim) Elem<T>::store(static_cast<T*>(a.out) + ((size_t)b * a.hq + h0 + r) * a.dim + d, o / l);
+    // the piece that starts at its unit's start lies in its CTA's second slot
+    auto piece = [&](int c) { return pieces + (size_t)(2 * c + (c == c0 ? 1 : 0)) * kPiece<kUnitRows>; };
+    float top = neg_inf();
+    for (int c = c0 + d; c <= c1; c += kMixMaxDim) top = fmaxf(top, piece(c)[kUnitRows * kMixMaxDim + r]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if ((d & 31) == 0) red[0][d >> 5] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kMixMaxDim / 32; ++w) top = fmaxf(top, red[0][w]);
+    const float base = top == neg_inf() ? 0.f : top;
+    float l = 0.f;
+    for (int c = c0 + d; c <= c1; c += kMixMaxDim) {
+        const float* p = piece(c) + kUnitRows * kMixMaxDim;
+        const float w = exp2f(p[r] - base);
+        weight[c - c0] = w;
+        l = fmaf(w, p[kUnitRows + r], l);
     }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    if ((d & 31) == 0) red[1][d >> 5] = l;
+    __syncthreads();
+    if (d >= a.dim) return;
+    l = red[1][0];
+#pragma unroll
+    for (int w = 1; w < kMixMaxDim / 32; ++w) l += red[1][w];
+    float o = piece(c0)[r * kMixMaxDim + d] * weight[0];
+#pragma unroll 8
+    for (int c = c0 + 1; c <= c1; ++c)
+        o = fmaf(pieces[(size_t)(2 * c) * kPiece<kUnitRows> + r * kMixMaxDim + d], weight[c - c0], o);
+    Elem<T>::store(static_cast<T*>(a.out) + ((size_t)b * a.hq + h) * a.dim + d, o / l);
 }
 
 // CTAs of the decode kernel: as many as fit the GPU at once, no more than there can be tiles.
@@ -613,9 +632,8 @@ bool cache_map(CUtensorMap* m, const void* p, const AttnDecodeArgs& a)
 template <typename T, int kUnitRows>
 cudaError_t launch_join(const AttnDecodeArgs& a, const float* pieces, int G, cudaStream_t s)
 {
-    const Units un(a.hq, a.hkv, kUnitRows);
-    return launch_dependent(attn_decode_join_kernel<T, kUnitRows>, dim3((unsigned)(a.batch * un.per_row)), dim3(kMixMaxDim), 0, s,
-                            a, pieces, G);
+    return launch_dependent(attn_decode_join_kernel<T, kUnitRows>, dim3((unsigned)(a.batch * a.hq)), dim3(kMixMaxDim),
+                            (size_t)G * sizeof(float), s, a, pieces, G);
 }
 
 template <int D, bool kHigh>
