@@ -8,6 +8,7 @@ is raised.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -366,34 +367,41 @@ def ssd_gdn_decode_step(state, q, k, v, gate, beta, out=None, stream=None):
 def _packed(t: torch.Tensor) -> int:
     """Elements from one token of ``t`` [tokens][heads][dim] to the next, for a tensor whose
     tokens may lie apart (a slice of a fused projection); each token's own elements may not."""
-    heads, dim = t.shape[1], t.shape[2]
-    if t.numel() and ((dim > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != dim)):
+    (tokens, heads, dim), (apart, head, one) = t.shape, t.stride()
+    if t.numel() and ((dim > 1 and one != 1) or (heads > 1 and head != dim)):
         raise ValueError("the heads of a token must be contiguous")
-    return t.stride(0) if t.shape[0] > 1 else heads * dim
+    return apart if tokens > 1 else heads * dim
 
 
 def _nseq(cu_seqlens: torch.Tensor) -> int:
-    if cu_seqlens.numel() < 2:
+    n = cu_seqlens.numel()
+    if n < 2:
         raise ValueError("cu_seqlens holds nseq + 1 offsets, at least two")
-    return cu_seqlens.numel() - 1
+    return n - 1
 
 
 def _check_mixer(ref: torch.Tensor, strided, specs):
     """_check_args for calls some of whose tensors (``strided``: tensor, name, shape) may have
-    their tokens apart."""
+    their tokens apart; those are of ``ref``'s dtype."""
     for t, name, shape in strided:
         if t.shape != shape:
             raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     _check_args(ref, specs)
+    dtype, device = ref.dtype, ref.get_device()
     for t, name, _ in strided:
-        if t.is_cuda and t.dtype == ref.dtype and t.get_device() == ref.get_device():
+        if t.dtype == dtype and t.get_device() == device and t.is_cuda:
             continue
         if not t.is_cuda:
             raise ValueError(f"{name} must be a CUDA tensor")
-        if t.dtype != ref.dtype:
-            raise TypeError(f"{name} must be {ref.dtype}")
-        if t.device != ref.device:
-            raise ValueError(f"{name} is on {t.device}, expected {ref.device}")
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}")
+        raise ValueError(f"{name} is on {t.device}, expected {ref.device}")
+
+
+@functools.lru_cache(maxsize=256)
+def _workspace_bytes(entry: str, *sizes) -> int:
+    """Workspace of a call: a function of its sizes alone."""
+    return int(getattr(lib(), entry)(*sizes))
 
 
 def ssd_linattn_prefill(q, k, v, log_decay, cu_seqlens, scale=1.0, init_states=None, out=None, final_states=None,
@@ -409,20 +417,20 @@ def ssd_linattn_prefill(q, k, v, log_decay, cu_seqlens, scale=1.0, init_states=N
     total, hq, dk = q.shape
     hv, dv = v.shape[1], v.shape[2]
     nseq = _nseq(cu_seqlens)
-    f32, state_shape = torch.float32, (nseq, hv, dk, dv)
-    _check_mixer(q, ((q, "q", q.shape), (k, "k", q.shape), (v, "v", (total, hv, dv))),
-                 ((log_decay, "log_decay", (hv,), f32), (cu_seqlens, "cu_seqlens", cu_seqlens.shape, torch.int32),
-                  (init_states, "init_states", state_shape, f32), (out, "out", (total, hv, dv), q.dtype),
+    f32, key_shape, out_shape, state_shape = torch.float32, (total, hq, dk), (total, hv, dv), (nseq, hv, dk, dv)
+    _check_mixer(q, ((q, "q", key_shape), (k, "k", key_shape), (v, "v", out_shape)),
+                 ((log_decay, "log_decay", (hv,), f32), (cu_seqlens, "cu_seqlens", (nseq + 1,), torch.int32),
+                  (init_states, "init_states", state_shape, f32), (out, "out", out_shape, q.dtype),
                   (final_states, "final_states", state_shape, f32),
                   (workspace, "workspace", workspace.shape if workspace is not None else (), None)))
     code = _dtype_code(q)
     if out is None:
-        out = torch.empty((total, hv, dv), device=q.device, dtype=q.dtype)
+        out = torch.empty(out_shape, dtype=q.dtype, device=q.device)
     if final_states is None:
-        final_states = torch.empty(state_shape, device=q.device, dtype=f32)
+        final_states = torch.empty(state_shape, dtype=f32, device=q.device)
     if workspace is None:
-        need = int(lib().ssd_linattn_prefill_workspace_bytes(nseq, total, hq, hv, dk, dv, code))
-        workspace = torch.empty(max(need, 16), device=q.device, dtype=torch.uint8)
+        need = _workspace_bytes("ssd_linattn_prefill_workspace_bytes", nseq, total, hq, hv, dk, dv, code)
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     st = lib().ssd_linattn_prefill(_ptr(q), _ptr(k), _ptr(v), _packed(q), _packed(k), _packed(v), _ptr(log_decay),
                                    _ptr(init_states), _ptr(cu_seqlens), nseq, total, hq, hv, dk, dv, scale, code,
                                    _ptr(out), _ptr(final_states), _ptr(workspace), _nbytes(workspace), _stream(stream))
@@ -438,10 +446,10 @@ def ssd_linattn_decode_step(state, q, k, v, log_decay, scale=1.0, out=None, stre
     _rank(v, "v", "[batch][heads_v][dv]")
     batch, hq, dk = q.shape
     hv, dv = v.shape[1], v.shape[2]
-    f32 = torch.float32
-    _check_args(q, ((state, "state", (batch, hv, dk, dv), f32), (q, "q", q.shape, q.dtype),
-                    (k, "k", q.shape, q.dtype), (v, "v", (batch, hv, dv), q.dtype),
-                    (log_decay, "log_decay", (hv,), f32), (out, "out", (batch, hv, dv), q.dtype)))
+    f32, dtype, key_shape, out_shape = torch.float32, q.dtype, (batch, hq, dk), (batch, hv, dv)
+    _check_args(q, ((state, "state", (batch, hv, dk, dv), f32), (q, "q", key_shape, dtype),
+                    (k, "k", key_shape, dtype), (v, "v", out_shape, dtype),
+                    (log_decay, "log_decay", (hv,), f32), (out, "out", out_shape, dtype)))
     if out is None:
         out = torch.empty_like(v)
     st = lib().ssd_linattn_decode_step(_ptr(state), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), batch, hq, hv, dk, dv,
@@ -460,11 +468,12 @@ def ssd_attn_prefill(q, k, v, cu_seqlens, scale=None, out=None, stream=None):
     _rank(cu_seqlens, "cu_seqlens", "[nseq + 1]")
     total, hq, dim = q.shape
     hkv, nseq = k.shape[1], _nseq(cu_seqlens)
-    _check_mixer(q, ((q, "q", q.shape), (k, "k", (total, hkv, dim)), (v, "v", (total, hkv, dim))),
-                 ((cu_seqlens, "cu_seqlens", cu_seqlens.shape, torch.int32), (out, "out", q.shape, q.dtype)))
+    out_shape, key_shape = (total, hq, dim), (total, hkv, dim)
+    _check_mixer(q, ((q, "q", out_shape), (k, "k", key_shape), (v, "v", key_shape)),
+                 ((cu_seqlens, "cu_seqlens", (nseq + 1,), torch.int32), (out, "out", out_shape, q.dtype)))
     code = _dtype_code(q)
     if out is None:
-        out = torch.empty(q.shape, device=q.device, dtype=q.dtype)
+        out = torch.empty(out_shape, dtype=q.dtype, device=q.device)
     st = lib().ssd_attn_prefill(_ptr(q), _ptr(k), _ptr(v), _packed(q), _packed(k), _packed(v), _ptr(cu_seqlens),
                                 nseq, total, hq, hkv, dim, dim ** -0.5 if scale is None else scale,
                                 code, _ptr(out), _stream(stream))
@@ -481,18 +490,18 @@ def ssd_attn_decode_step(k_cache, v_cache, cache_lens, q, k, v, scale=None, out=
     _rank(q, "q", "[batch][heads_q][headdim]")
     _rank(k_cache, "k_cache", "[batch][capacity][heads_kv][headdim]")
     batch, hq, dim = q.shape
-    capacity, hkv = k_cache.shape[1], k_cache.shape[2]
-    cache, new = (batch, capacity, hkv, dim), (batch, hkv, dim)
-    _check_args(q, ((k_cache, "k_cache", cache, q.dtype), (v_cache, "v_cache", cache, q.dtype),
-                    (cache_lens, "cache_lens", (batch,), torch.int32), (q, "q", q.shape, q.dtype),
-                    (k, "k", new, q.dtype), (v, "v", new, q.dtype), (out, "out", q.shape, q.dtype),
+    _, capacity, hkv, _ = k_cache.shape
+    dtype, cache, new, rows = q.dtype, (batch, capacity, hkv, dim), (batch, hkv, dim), (batch, hq, dim)
+    _check_args(q, ((k_cache, "k_cache", cache, dtype), (v_cache, "v_cache", cache, dtype),
+                    (cache_lens, "cache_lens", (batch,), torch.int32), (q, "q", rows, dtype),
+                    (k, "k", new, dtype), (v, "v", new, dtype), (out, "out", rows, dtype),
                     (workspace, "workspace", workspace.shape if workspace is not None else (), None)))
     code = _dtype_code(q)
     if out is None:
         out = torch.empty_like(q)
     if workspace is None:
-        need = int(lib().ssd_attn_decode_workspace_bytes(batch, capacity, hq, hkv, dim, code))
-        workspace = torch.empty(max(need, 16), device=q.device, dtype=torch.uint8)
+        need = _workspace_bytes("ssd_attn_decode_workspace_bytes", batch, capacity, hq, hkv, dim, code)
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     st = lib().ssd_attn_decode_step(_ptr(k_cache), _ptr(v_cache), _ptr(cache_lens), _ptr(q), _ptr(k), _ptr(v), batch,
                                     capacity, hq, hkv, dim, dim ** -0.5 if scale is None else scale, code, _ptr(out),
                                     _ptr(workspace), _nbytes(workspace), _stream(stream))
