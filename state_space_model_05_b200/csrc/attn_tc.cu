@@ -9,14 +9,15 @@
 // tile small.  Keys are visited 128 at a time.  Per key tile i and query tile j:
 //     S = Q_j K_i^T  (TMEM)  ->  softmax warps: row maximum, P = 2^(c S - m) as bf16 over S
 //     O_j += P V_i   (TMEM, A operand from TMEM)
-// Roles: four softmax warps per query tile (one thread per row), one issuing warp per query
-// tile, one TMA warp and one warp that looks after the values of the masked key tiles.  While
-// one tile's softmax runs, the tensor cores work for the other tile.
+// Roles: four softmax warps per query tile (one thread per row), one warp that issues each
+// tile's products, one TMA warp and one warp that looks after the values of the masked key tiles.
+// While one tile's softmax runs, the tensor cores work for the other tile: the tiles take turns
+// at the exponentials, since side by side both would wait for those and then for the products.
 //
 // The running maximum moves only when a row's scores exceed it by 2^8: until then p stays
 // below 2^8 and nothing has to be rescaled; the sum and O use the same m, so the quotient is
-// exact.  A move rescales O in TMEM by its own warp, which is safe because S_i is issued
-// only after P V_(i-1) has completed.  P is rounded to bf16 (the operand type; its sum is
+// exact.  A move rescales O in TMEM by its own warp, which is safe because the barrier that
+// announces S_i also covers P V_(i-1), issued before it.  P is rounded to bf16 (the operand type; its sum is
 // taken before the rounding, in fp32), as is the output; everything else is fp32.
 #include <cuda.h>
 
@@ -46,7 +47,7 @@ struct Cfg {
     static constexpr int kSlots = D == 128 ? 5 : 8;        // K and V tiles in flight
     static constexpr int kKv = 2 * kTile;
     static constexpr int kBar = kKv + kSlots * kTile;
-    static constexpr int kNumBars = 1 + 2 * kSlots + 6 + 2 * kMaxMasked;
+    static constexpr int kNumBars = 1 + 2 * kSlots + 8 + 2 * kMaxMasked;
     static constexpr int kTm = kBar + kNumBars * 8;
     static constexpr int kBytes = kTm + 16 + 1024;
     // TMEM columns: two score tiles, two outputs
@@ -80,12 +81,13 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b)
 // finite among the others: 0 x inf would carry them into rows that must not see them.  Those
 // are zeroed too and reported, and the epilogue adds them where they belong.
 template <int D>
-__device__ bool fix_values(uint8_t* sv, int rows, int lane)
+__device__ __forceinline__ bool fix_values(uint8_t* sv, int rows, int lane)
 {
     constexpr int kChunks = D / 8;                         // 16-byte chunks per row
     uint32_t bad = 0;
     const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
     __nv_bfloat162 acc = zero;
+#pragma unroll 4
     for (int i = lane; i < kKeys * kChunks; i += 32) {
         const int r = (i / 8) % kKeys;                     // halves of [128 rows][8 chunks]
         uint4* p = reinterpret_cast<uint4*>(sv) + i;       // (the swizzle permutes chunks within a row)
@@ -101,6 +103,7 @@ __device__ bool fix_values(uint8_t* sv, int rows, int lane)
     bad = __hisnan(acc.x) || __hisnan(acc.y);
     const bool any = __any_sync(0xffffffffu, bad);
     if (any) {
+#pragma unroll 1
         for (int i = lane; i < kKeys * kChunks; i += 32) {
             uint4* p = reinterpret_cast<uint4*>(sv) + i;
             uint4 u = *p;
@@ -116,6 +119,96 @@ __device__ bool fix_values(uint8_t* sv, int rows, int lane)
     return any;
 }
 
+// One row's softmax over one key tile: maximum, then P as bf16 over the scores in two parts
+// of 64 keys, announced on p_full[0] and p_full[1]; m and l are the row's running maximum and sum.
+// kAny: keys past `limit` are masked, and the scores scaled first when the scale is not positive.
+// turn / next: named barriers before and after the exponentials (0: none).
+template <int D, bool kAny>
+__device__ __forceinline__ void row_tile(uint32_t tS, uint32_t tO, bool started, float c, bool positive, int limit, float& m,
+                                         float& l, uint64_t* p_full, int turn, int next)
+{
+    constexpr float kNone = -__builtin_inff();
+    const float mul = !kAny || positive ? c : 1.f;
+    uint32_t a[32], b[32];
+    auto scores = [&](uint32_t (&s)[32], int e0) {
+        if (!kAny) return;
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+            float x = __uint_as_float(s[e]);
+            if (!positive) x *= c;
+            s[e] = __float_as_uint(e0 + e <= limit ? x : kNone);
+        }
+    };
+    float top[4] = {kNone, kNone, kNone, kNone};
+    auto maximum = [&](uint32_t (&s)[32], int e0) {
+        scores(s, e0);
+#pragma unroll
+        for (int e = 0; e < 32; e += 8)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) top[q] = max3(top[q], __uint_as_float(s[e + 2 * q]), __uint_as_float(s[e + 2 * q + 1]));
+    };
+    tmem_ld32(tS, a);
+#pragma unroll 1
+    for (int q = 0; q < 4; q += 2) {
+        tmem_wait_ld();
+        tmem_ld32(tS + 32 * q + 32, b);
+        maximum(a, 32 * q);
+        tmem_wait_ld();
+        tmem_ld32(tS + (q == 0 ? 64 : 0), a);              // in the end the first ones again
+        maximum(b, 32 * q + 32);
+    }
+    const float now = fmaxf(max3(top[0], top[1], top[2]), top[3]) * mul;
+    float keep = 1.f;
+    if (now > m + kSlack) {
+        keep = ex2(m - now);                               // 0 from the initial -inf
+        m = now;
+        l *= keep;
+    }
+    if (started && __any_sync(0xffffffffu, keep != 1.f)) {
+#pragma unroll 1
+        for (int q = 0; q < D / 32; ++q) {
+            tmem_ld32(tO + 32 * q, b);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) b[e] = __float_as_uint(__uint_as_float(b[e]) * keep);
+            tmem_st16(tO + 32 * q, reinterpret_cast<uint32_t(&)[16]>(b[0]));
+            tmem_st16(tO + 32 * q + 16, reinterpret_cast<uint32_t(&)[16]>(b[16]));
+        }
+    }
+    const float base = m == kNone ? 0.f : m;               // a row of -inf so far keeps p = 0
+    const float2 mul2 = make_float2(mul, mul), base2 = make_float2(-base, -base);
+    float2 sum[2] = {make_float2(l, 0.f), make_float2(0.f, 0.f)};
+    if (turn) named_bar_sync(turn, 2 * kRows);
+    auto probabilities = [&](uint32_t (&s)[32], int e0) {
+        scores(s, e0);
+        uint32_t p[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            float2 y = ffma2(make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), mul2, base2);
+            y.x = ex2(y.x);
+            y.y = ex2(y.y);
+            sum[e & 1] = add2(sum[e & 1], y);
+            p[e] = pack_bf16x2(y.x, y.y);
+        }
+        tmem_st16(tS + e0 / 2, p);
+    };
+#pragma unroll 1
+    for (int q = 0; q < 4; q += 2) {
+        tmem_wait_ld();
+        tmem_ld32(tS + 32 * q + 32, b);
+        probabilities(a, 32 * q);
+        tmem_wait_ld();
+        if (q == 0) tmem_ld32(tS + 64, a);
+        probabilities(b, 32 * q + 32);
+        if (q == 2 && next) named_bar_arrive(next, 2 * kRows);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&p_full[q >> 1]);
+    }
+    const float2 both = add2(sum[0], sum[1]);
+    l = both.x + both.y;
+}
+
 struct AttnMaps { CUtensorMap q, k, v; };
 
 template <int D>
@@ -127,7 +220,7 @@ attn_prefill_tc_kernel(const __grid_constant__ AttnMaps maps, const AttnArgs a, 
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::kBar);
     uint64_t *q_full = bars, *full = bars + 1, *empty = full + L::kSlots, *s_full = empty + L::kSlots,
-             *p_full = s_full + 2, *pv_done = p_full + 2, *v_in = pv_done + 2, *v_ok = v_in + kMaxMasked;
+             *p_full = s_full + 2, *o_full = p_full + 4, *v_in = o_full + 2, *v_ok = v_in + kMaxMasked;
     uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + L::kTm);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L::kTm + 4);
     int* bad_tiles = reinterpret_cast<int*>(sm + L::kTm + 8);
@@ -154,8 +247,9 @@ attn_prefill_tc_kernel(const __grid_constant__ AttnMaps maps, const AttnArgs a, 
         }
         for (int j = 0; j < 2; ++j) {
             mbar_init(&s_full[j], 1);
-            mbar_init(&p_full[j], kRows);
-            mbar_init(&pv_done[j], 1);
+            mbar_init(&p_full[2 * j], kRows);
+            mbar_init(&p_full[2 * j + 1], kRows);
+            mbar_init(&o_full[j], 1);
         }
         for (int i = 0; i < kMaxMasked; ++i) {
             mbar_init(&v_in[i], 1);
@@ -175,6 +269,7 @@ attn_prefill_tc_kernel(const __grid_constant__ AttnMaps maps, const AttnArgs a, 
     const uint32_t tmem = *tslot;
     auto kv = [&](int n) { return sm + L::kKv + (n % L::kSlots) * L::kTile; };   // K_i is tile 2 i, V_i tile 2 i + 1
     auto wait = [&](uint64_t* bar, int phase) { return mbar_wait_or_abort(bar, phase & 1, err, abort_flag); };
+    auto poll = [&](uint64_t* bar, int phase) { return mbar_poll_or_abort(bar, phase & 1, err, abort_flag); };
 
     if (warp == kWarpTma) {
         if (lane == 0) {
@@ -197,47 +292,55 @@ attn_prefill_tc_kernel(const __grid_constant__ AttnMaps maps, const AttnArgs a, 
             }
         }
     } else if (warp == kWarpMma || warp == kWarpMma + 1) {
+        // A thread per query tile issues that tile's products: most of a thread's time goes into
+        // the waits between them, which the other tile's products fill.
         if (lane == 0) {
-            const int j = warp - kWarpMma, n_own = j ? nk1 : nk0;
-            const uint32_t tS = tmem + L::kS + j * 128, tO = tmem + L::kO + j * 128;
             constexpr uint32_t idS = idesc_bf16_f32(128, kKeys, false, false);
             constexpr uint32_t idO = idesc_bf16_f32(128, D, false, true);
+            const int j = warp - kWarpMma, own = j ? nk1 : nk0;
+            const uint32_t tS = tmem + L::kS + j * 128, tO = tmem + L::kO + j * 128;
             const uint64_t dQ = smem_desc_sw128(smem_u32(sm + j * L::kTile), 16, 1024);
-            bool ok = n_own == 0 || wait(q_full, 0);
-            for (int i = 0; i < nk && ok; ++i) {
-                const int nK = 2 * i, nV = 2 * i + 1, sK = nK % L::kSlots, sV = nV % L::kSlots;
-                ok = wait(&full[sK], nK / L::kSlots);
-                if (!ok) break;
-                if (i >= n_own) {                          // a tile that only the other query tile needs
-                    mbar_arrive(&empty[sK]);
-                    ok = wait(&full[sV], nV / L::kSlots);
-                    mbar_arrive(&empty[sV]);
-                    continue;
-                }
-                // S over P: the product that reads P has to be complete
-                ok = i == 0 || wait(&pv_done[j], i - 1);
-                if (!ok) break;
-                tc_fence_after();
+            bool ok = own == 0 || poll(q_full, 0);
+#pragma unroll 1
+            for (int i = -1; i < nk && ok; ++i) {
+                // V_i and K_(i+1), waited for before P_i is
+                const int nV = 2 * i + 1, nK = 2 * i + 2;
+                const bool has_v = i >= 0, has_k = i + 1 < nk;
+                if (has_v) ok = poll(&full[nV % L::kSlots], nV / L::kSlots);
+                if (has_k) ok = ok && poll(&full[nK % L::kSlots], nK / L::kSlots);
                 const uint64_t dK = smem_desc_sw128(smem_u32(kv(nK)), 16, 1024);
-#pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks) {
-                    const uint32_t off = (ks >> 2) * kHalf + (ks & 3) * 32;
-                    umma_f16(tS, desc_advance(dQ, off), desc_advance(dK, off), idS, ks > 0 ? 1u : 0u);
-                }
-                umma_commit(&empty[sK]);
-                umma_commit(&s_full[j]);
-                ok = wait(&full[sV], nV / L::kSlots) && (i < masked || wait(&v_ok[i - masked], 0)) && wait(&p_full[j], i);
-                if (!ok) break;
-                tc_fence_after();
                 const uint64_t dV = smem_desc_sw128(smem_u32(kv(nV)), kHalf, 1024);
+                if (has_v && i < own) {                    // O += P V_i, P in two parts of 64 keys
+                    if (i >= masked) ok = ok && poll(&v_ok[i - masked], 0);
+#pragma unroll 1
+                    for (int part = 0; part < 2; ++part) {
+                        ok = ok && poll(&p_full[2 * j + part], i);
+                        if (!ok) break;
+                        tc_fence_after();
 #pragma unroll
-                for (int ks = 0; ks < kKeys / 16; ++ks)
-                    umma_f16_ts(tO, tS + ks * 8, desc_advance(dV, ks * 2048), idO, (i > 0 || ks > 0) ? 1u : 0u);
-                umma_commit(&empty[sV]);
-                umma_commit(&pv_done[j]);
+                        for (int ks = 0; ks < kKeys / 32; ++ks)
+                            umma_f16_ts(tO, tS + part * 32 + ks * 8, desc_advance(dV, part * 8192 + ks * 2048), idO,
+                                        (i > 0 || part > 0 || ks > 0) ? 1u : 0u);
+                    }
+                }
+                if (!ok) break;
+                if (i + 1 < own) {                         // S = Q K_(i+1)^T
+                    // S over P: products of one thread run in the order of issue, so the one that
+                    // reads P is done with it
+                    if (i < 0) tc_fence_after();
+#pragma unroll
+                    for (int ks = 0; ks < D / 16; ++ks) {
+                        const uint32_t off = (ks >> 2) * kHalf + (ks & 3) * 32;
+                        umma_f16(tS, desc_advance(dQ, off), desc_advance(dK, off), idS, ks > 0 ? 1u : 0u);
+                    }
+                    umma_commit(&s_full[j]);
+                }
+                if (i == own - 1 && own > 0) umma_commit(o_full + j);
+                if (has_v) umma_commit(&empty[nV % L::kSlots]);
+                if (has_k) umma_commit(&empty[nK % L::kSlots]);
             }
             // no TMEM is released with products in flight
-            if (ok && n_own > 0) wait(&pv_done[j], n_own - 1);
+            if (ok && own > 0) wait(&o_full[j], 0);
         }
     } else if (warp == kWarpValues) {
         for (int i = masked; i < nk; ++i) {
@@ -257,82 +360,37 @@ attn_prefill_tc_kernel(const __grid_constant__ AttnMaps maps, const AttnArgs a, 
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + lanes + L::kS + j * 128, tO = tmem + lanes + L::kO + j * 128;
         const float c = a.scale * kLog2e;
-        const bool positive = c > 0.f;
-        const float mul = positive ? c : 1.f;              // else the scores are scaled before the maximum
+        const bool positive = c > 0.f;                     // else the scores are scaled before the maximum
         float m = __int_as_float(0xff800000), l = 0.f;
         bool ok = true;
+        // turns at the exponentials: tile 0 first, then 1, .. while both have key tiles left.  (A
+        // thread that gives up a wait still takes its turns.)
+        if (j == 1 && nk1 > 0) named_bar_arrive(1, 2 * kRows);
         for (int i = 0; i < n_own; ++i) {
-            ok = __all_sync(0xffffffffu, wait(&s_full[j], i));
-            if (!ok) break;
+            const int turn = nk1 > 0 && i < nk0 ? 1 + j : 0;
+            const int next = nk1 > 0 && (j == 0 || i + 1 < nk0) ? 2 - j : 0;
+            ok = ok && __all_sync(0xffffffffu, wait(&s_full[j], i));
+            if (!ok) {
+                if (turn) named_bar_sync(turn, 2 * kRows);
+                if (next) named_bar_arrive(next, 2 * kRows);
+                continue;
+            }
             tc_fence_after();
-            uint32_t s[128];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) tmem_ld32(tS + 32 * q, reinterpret_cast<uint32_t(&)[32]>(s[32 * q]));
-            tmem_wait_ld();
-            float* x = reinterpret_cast<float*>(s);
-            if (!positive) {
-#pragma unroll
-                for (int e = 0; e < 128; ++e) x[e] *= c;
+            // (scores are read from TMEM twice, 32 at a time, rather than held: the loops stay small
+            // enough that the issuing warp's own instructions are not crowded out of the cache)
+            if (positive && i < masked) {
+                row_tile<D, false>(tS, tO, i > 0, c, false, kKeys, m, l, &p_full[2 * j], turn, next);
+            } else {
+                row_tile<D, true>(tS, tO, i > 0, c, positive, t - i * kKeys, m, l, &p_full[2 * j], turn, next);
             }
-            if (i >= masked) {
-                const int limit = t - i * kKeys;           // keys past the row's own token
-#pragma unroll
-                for (int e = 0; e < 128; ++e) x[e] = e <= limit ? x[e] : __int_as_float(0xff800000);
-            }
-            float top[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-            for (int e = 4; e < 128; e += 8) {
-#pragma unroll
-                for (int q = 0; q < 4; ++q) top[q] = e + q + 4 < 128 ? max3(top[q], x[e + q], x[e + q + 4]) : fmaxf(top[q], x[e + q]);
-            }
-            const float now = fmaxf(max3(top[0], top[1], top[2]), top[3]) * mul;
-            float keep = 1.f;
-            if (now > m + kSlack) {
-                keep = ex2(m - now);                       // 0 from the initial -inf
-                m = now;
-                l *= keep;
-            }
-            if (i > 0 && __any_sync(0xffffffffu, keep != 1.f)) {
-#pragma unroll
-                for (int q = 0; q < D / 32; ++q) {
-                    uint32_t o[32];
-                    tmem_ld32(tO + 32 * q, o);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
-                    tmem_st16(tO + 32 * q, reinterpret_cast<uint32_t(&)[16]>(o[0]));
-                    tmem_st16(tO + 32 * q + 16, reinterpret_cast<uint32_t(&)[16]>(o[16]));
-                }
-            }
-            const float base = m == __int_as_float(0xff800000) ? 0.f : m;   // a row of -inf so far keeps p = 0
-            const float2 mul2 = make_float2(mul, mul), base2 = make_float2(-base, -base);
-            float2 sum[2] = {make_float2(l, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                uint32_t p[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    float2 y = ffma2(make_float2(x[32 * q + 2 * e], x[32 * q + 2 * e + 1]), mul2, base2);
-                    y.x = ex2(y.x);
-                    y.y = ex2(y.y);
-                    sum[e & 1] = add2(sum[e & 1], y);
-                    p[e] = pack_bf16x2(y.x, y.y);
-                }
-                tmem_st16(tS + 16 * q, p);
-            }
-            const float2 both = add2(sum[0], sum[1]);
-            l = both.x + both.y;
-            tmem_wait_st();
-            tc_fence_before();
-            mbar_arrive(&p_full[j]);
         }
-        if (ok && n_own > 0 && __all_sync(0xffffffffu, wait(&pv_done[j], n_own - 1))) {
+        if (ok && n_own > 0 && __all_sync(0xffffffffu, wait(&o_full[j], 0))) {
             tc_fence_after();
             const float inv = 1.f / l;
             const int bad = *bad_tiles;
             __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) +
                                  ((size_t)(first + t) * a.hq + (size_t)hk * group + (r - tok * group)) * a.dim;
-#pragma unroll
+#pragma unroll 1
             for (int q = 0; q < D / 32; ++q) {
                 uint32_t o[32];
                 tmem_ld32(tO + 32 * q, o);
@@ -341,20 +399,22 @@ attn_prefill_tc_kernel(const __grid_constant__ AttnMaps maps, const AttnArgs a, 
                 float y[32];
 #pragma unroll
                 for (int e = 0; e < 32; ++e) y[e] = __uint_as_float(o[e]) * inv;
-                if (bad) {
-                    // values that are not finite, taken out of the product: p > 0 times one of
-                    // them is that value, whatever p is
-                    for (int i = masked; i < nk; ++i) {
-                        if (!(bad >> (i - masked) & 1)) continue;
-                        for (int s0 = i * kKeys; s0 <= min(t, i * kKeys + kKeys - 1); ++s0) {
-                            const __nv_bfloat16* vr = static_cast<const __nv_bfloat16*>(a.v) +
-                                                      (size_t)(first + s0) * a.v_stride + (size_t)hk * a.dim;
+                // values that are not finite, taken out of the product: p > 0 times one of them is
+                // that value, whatever p is
+                for (int i = masked; bad && i < nk; ++i) {
+                    if (!(bad >> (i - masked) & 1)) continue;
+#pragma unroll 1
+                    for (int s0 = i * kKeys; s0 <= min(t, i * kKeys + kKeys - 1); ++s0) {
+                        const uint4* vr = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.v) +
+                                                                         (size_t)(first + s0) * a.v_stride + (size_t)hk * a.dim + 32 * q);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                if (32 * q + e < a.dim) {
-                                    const float z = __bfloat162float(vr[32 * q + e]);
-                                    if (!(fabsf(z) < __int_as_float(0x7f800000))) y[e] += z;
-                                }
+                        for (int e = 0; e < 32; e += 8) {
+                            const uint4 u = 32 * q + e < a.dim ? vr[e / 8] : make_uint4(0u, 0u, 0u, 0u);
+                            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                            for (int z = 0; z < 8; ++z) {
+                                const float x = z & 1 ? bf16hi(w[z / 2]) : bf16lo(w[z / 2]);
+                                y[e + z] += fabsf(x) < __int_as_float(0x7f800000) ? 0.f : x;
                             }
                         }
                     }

@@ -49,16 +49,21 @@ struct AttnDecodeArgs {
 // least one number, and there are at most total / Q + nseq of them.
 __host__ __device__ inline int packed_blocks(int total, int nseq, int Q) { return total / Q + nseq; }
 
-// Sequence, block within it, first token and sequence length of block number i.  False (and
-// SSD_ERR_SHAPE in the error word) when the offsets around it are not a valid partition; a
-// true return may still name a block past its sequence's end (j * Q >= len).
+// Sequence, block within it, first token and sequence length of block number i, found by
+// whole warps (32 offsets per round of loads).  False (and SSD_ERR_SHAPE in the error word)
+// when the offsets around it are not a valid partition; a true return may still name a block
+// past its sequence's end (j * Q >= len).
 __device__ __forceinline__ bool packed_block(const int* __restrict__ cu, int nseq, int total, int Q, int i,
                                              int* err, int* seq, int* j, int* first, int* len)
 {
-    int lo = 0, hi = nseq - 1;                       // largest s with cu[s] / Q + s <= i
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (cu[mid] / Q + mid <= i) lo = mid; else hi = mid - 1;
+    const int lane = threadIdx.x & 31;
+    int lo = 0, n = nseq;                            // the largest s with cu[s] / Q + s <= i is in [lo, lo + n)
+    while (n > 1) {
+        const int step = (n + 31) / 32, s = lo + lane * step;
+        const unsigned below = __ballot_sync(0xffffffffu, lane * step < n && cu[s] / Q + s <= i);
+        const int k = below ? 31 - __clz(below) : 0;
+        lo += k * step;
+        n = min(step, n - k * step);
     }
     const int a = cu[lo], b = cu[lo + 1];
     if (a < 0 || b < a || b > total) {

@@ -77,6 +77,19 @@ __device__ __forceinline__ bool mbar_wait_or_abort(uint64_t* bar, uint32_t parit
     return false;
 }
 
+// The same wait polled with the non-blocking test, for threads whose waits are short and on
+// the critical path.
+__device__ __forceinline__ bool mbar_poll_or_abort(uint64_t* bar, uint32_t parity, int* err,
+                                                   volatile int* abort) {
+    for (uint32_t i = 0; i < (1u << 26); ++i) {
+        if (mbar_test_wait(bar, parity)) return true;
+        if ((i & 1023u) == 1023u && *abort) return false;
+    }
+    record_error(err, SSD_ERR_TIMEOUT);
+    *abort = 1;
+    return false;
+}
+
 // ---------------------------------------------------------------- dependent launch
 // Lets the next kernel of the stream (launched with programmatic stream serialisation)
 // be scheduled once every CTA of this grid has executed this or exited.
@@ -92,6 +105,11 @@ __device__ __forceinline__ void griddep_wait() {
 // ---------------------------------------------------------------- named barriers
 __device__ __forceinline__ void named_bar_sync(uint32_t id, uint32_t nthreads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
+}
+
+// Arrival at a named barrier that others of its `nthreads` threads wait at.
+__device__ __forceinline__ void named_bar_arrive(uint32_t id, uint32_t nthreads) {
+    asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
 
 // Named barrier over `nthreads` threads that also returns the AND of `pred` over them.
