@@ -41,7 +41,7 @@ __device__ __forceinline__ void fma4(float4& a, float s, const float4& b)
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
-attn_prefill_kernel(const AttnArgs a, int* err)
+attn_prefill_kernel(const AttnArgs a, const Divisor block, int* err)
 {
     extern __shared__ float sm[];
     float *sq = sm, *sk = sq + kTok * kLd, *sv = sk + kTok * kLd, *sp = sv + kTok * kLd;
@@ -49,7 +49,7 @@ attn_prefill_kernel(const AttnArgs a, int* err)
     if (blockIdx.x == 0 && h == 0) check_offsets(a.cu, a.nseq, a.total, err);
     int seq, j, first, len;
     // the blocks with the most keys first
-    if (!packed_block(a.cu, a.nseq, a.total, kTok, gridDim.x - 1 - blockIdx.x, err, &seq, &j, &first, &len)) return;
+    if (!packed_block(a.cu, a.nseq, a.total, block, gridDim.x - 1 - blockIdx.x, err, &seq, &j, &first, &len)) return;
     const int n = min(kTok, len - j * kTok);
     if (n <= 0) return;
     const size_t t0 = (size_t)first + (size_t)j * kTok;
@@ -155,7 +155,7 @@ cudaError_t prefill_t(const AttnArgs& a, cudaStream_t s)
     cudaError_t e = cudaFuncSetAttribute(attn_prefill_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)packed_blocks(a.total, a.nseq, kTok), (unsigned)a.hq);
-    attn_prefill_kernel<T><<<grid, kThreads, kBytes, s>>>(a, device_error_word());
+    attn_prefill_kernel<T><<<grid, kThreads, kBytes, s>>>(a, Divisor(kTok), device_error_word());
     return cudaGetLastError();
 }
 

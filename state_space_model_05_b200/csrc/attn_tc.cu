@@ -79,32 +79,41 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b)
 
 // Zeroes value rows from `rows` on (another sequence's) and looks for values that are not
 // finite among the others: 0 x inf would carry them into rows that must not see them.  Those
-// are zeroed too and reported, and the epilogue adds them where they belong.
+// are zeroed too and reported, and the epilogue adds them where they belong.  A lane takes one
+// 16-byte chunk of every fourth row (the swizzle permutes chunks within a row).
 template <int D>
 __device__ __forceinline__ bool fix_values(uint8_t* sv, int rows, int lane)
 {
-    constexpr int kChunks = D / 8;                         // 16-byte chunks per row
-    uint32_t bad = 0;
     const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
-    __nv_bfloat162 acc = zero;
-#pragma unroll 4
-    for (int i = lane; i < kKeys * kChunks; i += 32) {
-        const int r = (i / 8) % kKeys;                     // halves of [128 rows][8 chunks]
-        uint4* p = reinterpret_cast<uint4*>(sv) + i;       // (the swizzle permutes chunks within a row)
-        if (r >= rows) {
-            *p = make_uint4(0u, 0u, 0u, 0u);
-        } else {
-            const uint4 u = *p;
-            const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&u);
+    __nv_bfloat162 acc[4] = {zero, zero, zero, zero};      // NaN as soon as one of its values is not finite
+#pragma unroll 1
+    for (int h = 0; h < D / 64; ++h) {
+        uint4* p = reinterpret_cast<uint4*>(sv + h * kHalf) + lane;
+        const int full = rows / 4;                         // groups of four rows that all count
+#pragma unroll 8
+        for (int k = 0; k < full; ++k) {
+            const uint4 u = p[32 * k];
+            const __nv_bfloat162* x = reinterpret_cast<const __nv_bfloat162*>(&u);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) acc = __hfma2(h[j], zero, acc);
+            for (int j = 0; j < 4; ++j) acc[j] = __hfma2(x[j], zero, acc[j]);
+        }
+#pragma unroll 2
+        for (int k = full; k < kKeys / 4; ++k) {
+            if (4 * k + (lane >> 3) >= rows) {
+                p[32 * k] = make_uint4(0u, 0u, 0u, 0u);
+            } else {
+                const uint4 u = p[32 * k];
+                const __nv_bfloat162* x = reinterpret_cast<const __nv_bfloat162*>(&u);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[j] = __hfma2(x[j], zero, acc[j]);
+            }
         }
     }
-    bad = __hisnan(acc.x) || __hisnan(acc.y);
-    const bool any = __any_sync(0xffffffffu, bad);
+    const __nv_bfloat162 all = __hadd2(__hadd2(acc[0], acc[1]), __hadd2(acc[2], acc[3]));
+    const bool any = __any_sync(0xffffffffu, __hisnan(all.x) || __hisnan(all.y));
     if (any) {
 #pragma unroll 1
-        for (int i = lane; i < kKeys * kChunks; i += 32) {
+        for (int i = lane; i < kKeys * (D / 8); i += 32) {
             uint4* p = reinterpret_cast<uint4*>(sv) + i;
             uint4 u = *p;
             uint32_t* w = reinterpret_cast<uint32_t*>(&u);
@@ -119,45 +128,50 @@ __device__ __forceinline__ bool fix_values(uint8_t* sv, int rows, int lane)
     return any;
 }
 
+constexpr float kNone = -__builtin_inff();
+
+// One row's scores made ready for row_tile where they need it: keys past `limit` masked, and all
+// times `c` (whole: every score, not only where the mask reaches).  A short loop of its own, so that
+// row_tile's long code exists once: short prompts run it cold.
+__device__ __forceinline__ void prepare_scores(uint32_t tS, float c, bool whole, int limit)
+{
+#pragma unroll 1
+    for (int q = 0; q < kKeys / 32; ++q) {
+        const int first = 32 * q;
+        if (!whole && __all_sync(0xffffffffu, limit >= first + 31)) continue;
+        uint32_t s[32];
+        if (whole || __any_sync(0xffffffffu, limit >= first)) {
+            tmem_ld32(tS + first, s);
+            tmem_wait_ld();
+        }
+#pragma unroll
+        for (int e = 0; e < 32; ++e) s[e] = __float_as_uint(e <= limit - first ? __uint_as_float(s[e]) * c : kNone);
+        tmem_st16(tS + first, reinterpret_cast<uint32_t(&)[16]>(s[0]));
+        tmem_st16(tS + first + 16, reinterpret_cast<uint32_t(&)[16]>(s[16]));
+    }
+    tmem_wait_st();
+}
+
 // One row's softmax over one key tile: maximum, then P as bf16 over the scores in two parts
 // of 64 keys, announced on p_full[0] and p_full[1]; m and l are the row's running maximum and sum.
-// kAny: keys past `limit` are masked, and the scores scaled first when the scale is not positive.
 // turn / next: named barriers before and after the exponentials (0: none).
-template <int D, bool kAny>
-__device__ __forceinline__ void row_tile(uint32_t tS, uint32_t tO, bool started, float c, bool positive, int limit, float& m,
-                                         float& l, uint64_t* p_full, int turn, int next)
+template <int D>
+__device__ __forceinline__ void row_tile(uint32_t tS, uint32_t tO, bool started, float mul, float& m, float& l, uint64_t* p_full,
+                                         int turn, int next)
 {
-    constexpr float kNone = -__builtin_inff();
-    const float mul = !kAny || positive ? c : 1.f;
-    uint32_t a[32], b[32];
-    auto scores = [&](uint32_t (&s)[32], int e0) {
-        if (!kAny) return;
+    uint32_t s[kKeys];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-            float x = __uint_as_float(s[e]);
-            if (!positive) x *= c;
-            s[e] = __float_as_uint(e0 + e <= limit ? x : kNone);
-        }
-    };
-    float top[4] = {kNone, kNone, kNone, kNone};
-    auto maximum = [&](uint32_t (&s)[32], int e0) {
-        scores(s, e0);
+    for (int q = 0; q < 4; ++q) tmem_ld32(tS + 32 * q, reinterpret_cast<uint32_t(&)[32]>(s[32 * q]));
+    tmem_wait_ld();
+    float* x = reinterpret_cast<float*>(s);
+    float top[8];
 #pragma unroll
-        for (int e = 0; e < 32; e += 8)
+    for (int q = 0; q < 8; ++q) {
+        top[q] = fmaxf(x[q], x[q + 8]);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) top[q] = max3(top[q], __uint_as_float(s[e + 2 * q]), __uint_as_float(s[e + 2 * q + 1]));
-    };
-    tmem_ld32(tS, a);
-#pragma unroll 1
-    for (int q = 0; q < 4; q += 2) {
-        tmem_wait_ld();
-        tmem_ld32(tS + 32 * q + 32, b);
-        maximum(a, 32 * q);
-        tmem_wait_ld();
-        tmem_ld32(tS + (q == 0 ? 64 : 0), a);              // in the end the first ones again
-        maximum(b, 32 * q + 32);
+        for (int e = 16; e < kKeys; e += 16) top[q] = max3(top[q], x[e + q], x[e + q + 8]);
     }
-    const float now = fmaxf(max3(top[0], top[1], top[2]), top[3]) * mul;
+    const float now = max3(max3(top[0], top[1], top[2]), max3(top[3], top[4], top[5]), fmaxf(top[6], top[7])) * mul;
     float keep = 1.f;
     if (now > m + kSlack) {
         keep = ex2(m - now);                               // 0 from the initial -inf
@@ -166,44 +180,38 @@ __device__ __forceinline__ void row_tile(uint32_t tS, uint32_t tO, bool started,
     }
     if (started && __any_sync(0xffffffffu, keep != 1.f)) {
 #pragma unroll 1
-        for (int q = 0; q < D / 32; ++q) {
-            tmem_ld32(tO + 32 * q, b);
+        for (int q = 0; q < D / 16; ++q) {
+            uint32_t o[16];
+            tmem_ld16(tO + 16 * q, o);
             tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) b[e] = __float_as_uint(__uint_as_float(b[e]) * keep);
-            tmem_st16(tO + 32 * q, reinterpret_cast<uint32_t(&)[16]>(b[0]));
-            tmem_st16(tO + 32 * q + 16, reinterpret_cast<uint32_t(&)[16]>(b[16]));
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
+            tmem_st16(tO + 16 * q, o);
         }
     }
     const float base = m == kNone ? 0.f : m;               // a row of -inf so far keeps p = 0
     const float2 mul2 = make_float2(mul, mul), base2 = make_float2(-base, -base);
     float2 sum[2] = {make_float2(l, 0.f), make_float2(0.f, 0.f)};
     if (turn) named_bar_sync(turn, 2 * kRows);
-    auto probabilities = [&](uint32_t (&s)[32], int e0) {
-        scores(s, e0);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
         uint32_t p[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-            float2 y = ffma2(make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), mul2, base2);
+            const int k = 32 * q + 2 * e;
+            float2 y = ffma2(make_float2(x[k], x[k + 1]), mul2, base2);
             y.x = ex2(y.x);
             y.y = ex2(y.y);
             sum[e & 1] = add2(sum[e & 1], y);
             p[e] = pack_bf16x2(y.x, y.y);
         }
-        tmem_st16(tS + e0 / 2, p);
-    };
-#pragma unroll 1
-    for (int q = 0; q < 4; q += 2) {
-        tmem_wait_ld();
-        tmem_ld32(tS + 32 * q + 32, b);
-        probabilities(a, 32 * q);
-        tmem_wait_ld();
-        if (q == 0) tmem_ld32(tS + 64, a);
-        probabilities(b, 32 * q + 32);
+        tmem_st16(tS + 16 * q, p);
         if (q == 2 && next) named_bar_arrive(next, 2 * kRows);
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(&p_full[q >> 1]);
+        if (q & 1) {
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(&p_full[q >> 1]);
+        }
     }
     const float2 both = add2(sum[0], sum[1]);
     l = both.x + both.y;
@@ -211,9 +219,33 @@ __device__ __forceinline__ void row_tile(uint32_t tS, uint32_t tO, bool started,
 
 struct AttnMaps { CUtensorMap q, k, v; };
 
+// Adds to eight outputs of a row (from dimension d0) the values that are not finite and that its
+// token t may see, which were taken out of the masked key tiles named in `bad`: p > 0 times one
+// of them is that value, whatever p is.
+__device__ __noinline__ uint4 add_bad_values(const AttnArgs& a, uint4 out, int bad, int masked, int first, int t, int hk, int d0)
+{
+    uint32_t w[4] = {out.x, out.y, out.z, out.w};
+    for (int i = masked; bad >> (i - masked); ++i) {
+        if (!(bad >> (i - masked) & 1)) continue;
+        for (int s = i * kKeys; s <= min(t, i * kKeys + kKeys - 1); ++s) {
+            const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.v) +
+                                                            (size_t)(first + s) * a.v_stride + (size_t)hk * a.dim + d0);
+            const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float lo = bf16lo(x[e]), hi = bf16hi(x[e]), inf = __int_as_float(0x7f800000);
+                if (!(fabsf(lo) < inf) || !(fabsf(hi) < inf))
+                    w[e] = pack_bf16x2(bf16lo(w[e]) + (fabsf(lo) < inf ? 0.f : lo), bf16hi(w[e]) + (fabsf(hi) < inf ? 0.f : hi));
+            }
+        }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-attn_prefill_tc_kernel(const __grid_constant__ AttnMaps maps, const AttnArgs a, int* err)
+attn_prefill_tc_kernel(const __grid_constant__ AttnMaps maps, const AttnArgs a, int group, int span, const Divisor block_div,
+                       const Divisor hkv_div, int* err)
 {
     using L = Cfg<D>;
     extern __shared__ uint8_t smem_raw[];
@@ -226,75 +258,77 @@ attn_prefill_tc_kernel(const __grid_constant__ AttnMaps maps, const AttnArgs a, 
     int* bad_tiles = reinterpret_cast<int*>(sm + L::kTm + 8);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-    // this CTA's rows: blocks with the most keys first, the key/value heads side by side
-    const int group = a.hq / a.hkv, span = kRows / group;  // tokens per query tile
-    const int hk = blockIdx.x % a.hkv, blk = gridDim.x / a.hkv - 1 - blockIdx.x / a.hkv;
-    if (blockIdx.x == 0) check_offsets(a.cu, a.nseq, a.total, err);
-    int seq, j0, first, len;
-    if (!packed_block(a.cu, a.nseq, a.total, 2 * span, blk, err, &seq, &j0, &first, &len)) return;
-    const int t0 = j0 * 2 * span;                          // first token, within the sequence
-    if (t0 >= len) return;
-    // key tiles that each query tile needs; from `masked` on a tile reaches past some row's diagonal
-    const int nk0 = (min(t0 + span, len) - 1) / kKeys + 1;
-    const int nk1 = t0 + span < len ? (min(t0 + 2 * span, len) - 1) / kKeys + 1 : 0;
-    const int nk = max(nk0, nk1), masked = (t0 + 1) / kKeys;
-
-    if (tid == 0) {
-        mbar_init(q_full, 1);
-        for (int s = 0; s < L::kSlots; ++s) {
-            mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 2);
+    // barriers and TMEM while the offsets are on their way
+    if (warp == kWarpTma) {
+        if (lane < 3) prefetch_tensor_map(lane == 0 ? &maps.q : lane == 1 ? &maps.k : &maps.v);
+        static_assert(L::kNumBars <= 32, "a lane per barrier");
+        // arrivals per phase: two for the slots' release (a thread per query tile), a tile's rows for P
+        const int e = lane - (1 + L::kSlots), p = lane - (1 + 2 * L::kSlots + 2);
+        if (lane < L::kNumBars) mbar_init(&bars[lane], e >= 0 && e < L::kSlots ? 2 : p >= 0 && p < 4 ? kRows : 1);
+        if (lane == 0) {
+            *abort_flag = 0;
+            *bad_tiles = 0;
         }
-        for (int j = 0; j < 2; ++j) {
-            mbar_init(&s_full[j], 1);
-            mbar_init(&p_full[2 * j], kRows);
-            mbar_init(&p_full[2 * j + 1], kRows);
-            mbar_init(&o_full[j], 1);
-        }
-        for (int i = 0; i < kMaxMasked; ++i) {
-            mbar_init(&v_in[i], 1);
-            mbar_init(&v_ok[i], 1);
-        }
-        *abort_flag = 0;
-        *bad_tiles = 0;
         fence_mbar_init();
     }
     if (warp == kWarpMma) {
         tmem_alloc(tslot, 512);
         tmem_relinquish();
     }
+
+    // this CTA's rows: blocks with the most keys first, the key/value heads side by side
+    // (group: query heads per key/value head; span: tokens per query tile)
+    const int place = gridDim.x - 1 - blockIdx.x, blk = hkv_div.d > 1 ? hkv_div.div(place) : place, hk = place - blk * a.hkv;
+    if (blockIdx.x == 0) check_offsets(a.cu, a.nseq, a.total, err);
+    int seq, j0, first, len;
+    const bool valid = packed_block(a.cu, a.nseq, a.total, block_div, blk, err, &seq, &j0, &first, &len);
+    const int t0 = valid ? j0 * 2 * span : 0;              // first token, within the sequence
+    const bool work = valid && t0 < len;
+    // key tiles that each query tile needs; from `masked` on a tile reaches past some row's diagonal
+    const int nk0 = work ? (min(t0 + span, len) - 1) / kKeys + 1 : 0;
+    const int nk1 = work && t0 + span < len ? (min(t0 + 2 * span, len) - 1) / kKeys + 1 : 0;
+    const int nk = max(nk0, nk1), masked = (t0 + 1) / kKeys;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tslot;
     auto kv = [&](int n) { return sm + L::kKv + (n % L::kSlots) * L::kTile; };   // K_i is tile 2 i, V_i tile 2 i + 1
+    auto load = [&](int n) {
+        // a masked tile's values go to the values warp first: its barriers are used once, so that
+        // it need not follow the slots' phases (`full` then only marks the turn)
+        uint64_t* slot = &full[n % L::kSlots];
+        const bool to_fix = (n & 1) && (n >> 1) >= masked;
+        uint64_t* bar = to_fix ? &v_in[(n >> 1) - masked] : slot;
+        mbar_expect_tx(bar, L::kTile);
+        for (int h = 0; h < L::kHalves; ++h)
+            tma_load_3d(kv(n) + h * kHalf, n & 1 ? &maps.v : &maps.k, 64 * h, hk, first + (n >> 1) * kKeys, bar);
+        if (to_fix) mbar_arrive(slot);
+    };
+    const uint32_t tmem = *tslot;
     auto wait = [&](uint64_t* bar, int phase) { return mbar_wait_or_abort(bar, phase & 1, err, abort_flag); };
     auto poll = [&](uint64_t* bar, int phase) { return mbar_poll_or_abort(bar, phase & 1, err, abort_flag); };
 
+    // the softmax threads hold a row of scores each: 216 registers for them, 72 for the other
+    // warps (together the 384 x 168 that the CTA was launched with)
+    if (warp >= kWarpTma) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == kWarpTma) {
-        if (lane == 0) {
+        if (elect_one() && nk > 0) {
             const int tiles = nk1 > 0 ? 2 : 1;
             mbar_expect_tx(q_full, tiles * L::kHalves * 128 * group * span);
+#pragma unroll 1
             for (int j = 0; j < tiles; ++j)
                 for (int h = 0; h < L::kHalves; ++h)
                     tma_load_3d(sm + j * L::kTile + h * kHalf, &maps.q, 64 * h, hk * group, first + t0 + j * span, q_full);
+#pragma unroll 1
             for (int n = 0; n < 2 * nk; ++n) {
-                const int s = n % L::kSlots;
-                if (n >= L::kSlots && !wait(&empty[s], n / L::kSlots - 1)) break;
-                // a masked tile's values go to the values warp first: its barriers are used once,
-                // so that it need not follow the slots' phases (`full` then only marks the turn)
-                const bool to_fix = (n & 1) && (n >> 1) >= masked;
-                uint64_t* bar = to_fix ? &v_in[(n >> 1) - masked] : &full[s];
-                mbar_expect_tx(bar, L::kTile);
-                for (int h = 0; h < L::kHalves; ++h)
-                    tma_load_3d(kv(n) + h * kHalf, n & 1 ? &maps.v : &maps.k, 64 * h, hk, first + (n >> 1) * kKeys, bar);
-                if (to_fix) mbar_arrive(&full[s]);
+                if (n >= L::kSlots && !wait(&empty[n % L::kSlots], n / L::kSlots - 1)) break;
+                load(n);
             }
         }
     } else if (warp == kWarpMma || warp == kWarpMma + 1) {
         // A thread per query tile issues that tile's products: most of a thread's time goes into
         // the waits between them, which the other tile's products fill.
-        if (lane == 0) {
+        if (elect_one()) {
             constexpr uint32_t idS = idesc_bf16_f32(128, kKeys, false, false);
             constexpr uint32_t idO = idesc_bf16_f32(128, D, false, true);
             const int j = warp - kWarpMma, own = j ? nk1 : nk0;
@@ -351,8 +385,10 @@ attn_prefill_tc_kernel(const __grid_constant__ AttnMaps maps, const AttnArgs a, 
             __syncwarp();
             if (lane == 0) mbar_arrive(&v_ok[i - masked]);
         }
+    }
     } else {
         // ---------------------------------------------------------------- softmax
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         const int j = warp >> 2, r = tid & 127;            // query tile, row
         const int tok = r / group, t = t0 + j * span + tok;   // the row's token, within the sequence
         const bool live = tok < span && t < len;
@@ -360,7 +396,7 @@ attn_prefill_tc_kernel(const __grid_constant__ AttnMaps maps, const AttnArgs a, 
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + lanes + L::kS + j * 128, tO = tmem + lanes + L::kO + j * 128;
         const float c = a.scale * kLog2e;
-        const bool positive = c > 0.f;                     // else the scores are scaled before the maximum
+        const bool positive = c > 0.f;
         float m = __int_as_float(0xff800000), l = 0.f;
         bool ok = true;
         // turns at the exponentials: tile 0 first, then 1, .. while both have key tiles left.  (A
@@ -376,55 +412,55 @@ attn_prefill_tc_kernel(const __grid_constant__ AttnMaps maps, const AttnArgs a, 
                 continue;
             }
             tc_fence_after();
-            // (scores are read from TMEM twice, 32 at a time, rather than held: the loops stay small
-            // enough that the issuing warp's own instructions are not crowded out of the cache)
-            if (positive && i < masked) {
-                row_tile<D, false>(tS, tO, i > 0, c, false, kKeys, m, l, &p_full[2 * j], turn, next);
-            } else {
-                row_tile<D, true>(tS, tO, i > 0, c, positive, t - i * kKeys, m, l, &p_full[2 * j], turn, next);
-            }
+            // (a scale that is not positive is applied before the maximum)
+            if (i >= masked || !positive) prepare_scores(tS, positive ? 1.f : c, !positive, i < masked ? kKeys : t - i * kKeys);
+            row_tile<D>(tS, tO, i > 0, positive ? c : 1.f, m, l, &p_full[2 * j], turn, next);
         }
         if (ok && n_own > 0 && __all_sync(0xffffffffu, wait(&o_full[j], 0))) {
             tc_fence_after();
             const float inv = 1.f / l;
             const int bad = *bad_tiles;
-            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) +
-                                 ((size_t)(first + t) * a.hq + (size_t)hk * group + (r - tok * group)) * a.dim;
-#pragma unroll 1
+            // a row per thread goes through the query tile's memory (its products have completed), so
+            // that the global stores are whole rows: 16-byte chunks, permuted by the row
+            constexpr int kChunks = D / 8;
+            uint8_t* stage = sm + j * L::kTile + (warp & 3) * 32 * D * 2;
+#pragma unroll 1                                           // (code that runs once comes from far: loops, not copies)
             for (int q = 0; q < D / 32; ++q) {
                 uint32_t o[32];
                 tmem_ld32(tO + 32 * q, o);
                 tmem_wait_ld();
-                if (!live) continue;
                 float y[32];
 #pragma unroll
                 for (int e = 0; e < 32; ++e) y[e] = __uint_as_float(o[e]) * inv;
-                // values that are not finite, taken out of the product: p > 0 times one of them is
-                // that value, whatever p is
-                for (int i = masked; bad && i < nk; ++i) {
-                    if (!(bad >> (i - masked) & 1)) continue;
-#pragma unroll 1
-                    for (int s0 = i * kKeys; s0 <= min(t, i * kKeys + kKeys - 1); ++s0) {
-                        const uint4* vr = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.v) +
-                                                                         (size_t)(first + s0) * a.v_stride + (size_t)hk * a.dim + 32 * q);
-#pragma unroll
-                        for (int e = 0; e < 32; e += 8) {
-                            const uint4 u = 32 * q + e < a.dim ? vr[e / 8] : make_uint4(0u, 0u, 0u, 0u);
-                            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                            for (int z = 0; z < 8; ++z) {
-                                const float x = z & 1 ? bf16hi(w[z / 2]) : bf16lo(w[z / 2]);
-                                y[e + z] += fabsf(x) < __int_as_float(0x7f800000) ? 0.f : x;
-                            }
-                        }
-                    }
-                }
 #pragma unroll
                 for (int e = 0; e < 32; e += 8)
-                    if (32 * q + e < a.dim)
-                        *reinterpret_cast<uint4*>(out + 32 * q + e) =
-                            make_uint4(pack_bf16x2(y[e], y[e + 1]), pack_bf16x2(y[e + 2], y[e + 3]),
-                                       pack_bf16x2(y[e + 4], y[e + 5]), pack_bf16x2(y[e + 6], y[e + 7]));
+                    *reinterpret_cast<uint4*>(stage + lane * (D * 2) + (((4 * q + e / 8) ^ (lane & 7)) << 4)) =
+                        make_uint4(pack_bf16x2(y[e], y[e + 1]), pack_bf16x2(y[e + 2], y[e + 3]),
+                                   pack_bf16x2(y[e + 4], y[e + 5]), pack_bf16x2(y[e + 6], y[e + 7]));
+            }
+            __syncwarp();
+            // rows of the tile start at this (token, head); a row's place after it fits 32 bits
+            // (128 tokens of 65535 heads of 128)
+            const int to_row = live ? tok * a.hq + (r - tok * group) : -1;
+            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) +
+                                 ((size_t)(first + t0 + j * span) * a.hq + (size_t)hk * group) * a.dim;
+            if (bad) {
+                // (rare: the staged rows are corrected where they lie)
+#pragma unroll 1
+                for (int c8 = 0; 8 * c8 < a.dim; ++c8) {
+                    uint4* p = reinterpret_cast<uint4*>(stage + lane * (D * 2) + ((c8 ^ (lane & 7)) << 4));
+                    if (live) *p = add_bad_values(a, *p, bad, masked, first, t, hk, 8 * c8);
+                }
+                __syncwarp();
+            }
+            const int row0 = lane / kChunks, ch = lane % kChunks;
+            const bool inside = 8 * ch < a.dim;
+            out += 8 * ch;
+#pragma unroll 2
+            for (int k = 0; k < kChunks; ++k) {
+                const int row = k * (32 / kChunks) + row0, to = __shfl_sync(0xffffffffu, to_row, row);
+                const uint4 v = *reinterpret_cast<const uint4*>(stage + row * (D * 2) + ((ch ^ (row & 7)) << 4));
+                if (to >= 0 && inside) *reinterpret_cast<uint4*>(out + (size_t)(unsigned)(to * a.dim)) = v;
             }
         }
     }
@@ -459,7 +495,7 @@ cudaError_t launch_t(const AttnArgs& a, cudaStream_t s)
     if (e != cudaSuccess) return e;
     const long long grid = (long long)packed_blocks(a.total, a.nseq, 2 * span) * a.hkv;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
-    attn_prefill_tc_kernel<D><<<(unsigned)grid, kThreads, Cfg<D>::kBytes, s>>>(maps, a, device_error_word());
+    attn_prefill_tc_kernel<D><<<(unsigned)grid, kThreads, Cfg<D>::kBytes, s>>>(maps, a, group, span, Divisor(2 * span), Divisor(a.hkv), device_error_word());
     return cudaGetLastError();
 }
 

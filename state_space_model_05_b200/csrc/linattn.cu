@@ -119,14 +119,14 @@ __device__ __forceinline__ void fma4(float4& a, float s, const float4& b)
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
-linattn_block_state_kernel(const LinattnArgs a, float* __restrict__ states, int* err)
+linattn_block_state_kernel(const LinattnArgs a, const Divisor block, float* __restrict__ states, int* err)
 {
     extern __shared__ float sm[];
     float *sk = sm, *sv = sm + kTok * kLd;
     const int h = blockIdx.y, tid = threadIdx.x;
     if (blockIdx.x == 0 && h == 0) check_offsets(a.cu, a.nseq, a.total, err);
     int seq, j, first, len;
-    if (!packed_block(a.cu, a.nseq, a.total, kTok, blockIdx.x, err, &seq, &j, &first, &len)) return;
+    if (!packed_block(a.cu, a.nseq, a.total, block, blockIdx.x, err, &seq, &j, &first, &len)) return;
     const int n = min(kTok, len - j * kTok);
     if (n <= 0) return;
     const size_t t0 = (size_t)first + (size_t)j * kTok;
@@ -189,13 +189,13 @@ linattn_scan_kernel(const LinattnArgs a, float* __restrict__ states, int* err)
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
-linattn_block_output_kernel(const LinattnArgs a, const float* __restrict__ states, int* err)
+linattn_block_output_kernel(const LinattnArgs a, const Divisor block, const float* __restrict__ states, int* err)
 {
     extern __shared__ float sm[];
     float *sq = sm, *sk = sq + kTok * kLd, *sv = sk + kTok * kLd, *sp = sv + kTok * kLd;
     const int h = blockIdx.y, tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     int seq, j, first, len;
-    if (!packed_block(a.cu, a.nseq, a.total, kTok, blockIdx.x, err, &seq, &j, &first, &len)) return;
+    if (!packed_block(a.cu, a.nseq, a.total, block, blockIdx.x, err, &seq, &j, &first, &len)) return;
     const int n = min(kTok, len - j * kTok);
     if (n <= 0) return;
     const size_t t0 = (size_t)first + (size_t)j * kTok;
@@ -297,10 +297,10 @@ cudaError_t prefill_t(const LinattnArgs& a, float* states, cudaStream_t s)
     if (e != cudaSuccess) return e;
     int* err = device_error_word();
     const dim3 grid((unsigned)packed_blocks(a.total, a.nseq, kTok), (unsigned)a.hv);
-    linattn_block_state_kernel<T><<<grid, kThreads, kStateBytes, s>>>(a, states, err);
+    linattn_block_state_kernel<T><<<grid, kThreads, kStateBytes, s>>>(a, Divisor(kTok), states, err);
     const dim3 scan((unsigned)(a.nseq * a.hv), (unsigned)((a.dk * a.dv + 4 * kThreads - 1) / (4 * kThreads)));
     linattn_scan_kernel<<<scan, kThreads, 0, s>>>(a, states, err);
-    if (a.total > 0) linattn_block_output_kernel<T><<<grid, kThreads, kOutBytes, s>>>(a, states, err);
+    if (a.total > 0) linattn_block_output_kernel<T><<<grid, kThreads, kOutBytes, s>>>(a, Divisor(kTok), states, err);
     return cudaGetLastError();
 }
 

@@ -121,10 +121,10 @@ struct LinattnMaps { CUtensorMap q, k, v; };
 // The segment of this CTA: sequence, segment within it, its first token and number of tokens.
 struct Segment { int seq, j, first, start, len, seq_len; };
 
-__device__ __forceinline__ bool this_segment(const LinattnArgs& a, int blocks, int* err, Segment* s)
+__device__ __forceinline__ bool this_segment(const LinattnArgs& a, int blocks, const Divisor& len_div, int unit, int* err, Segment* s)
 {
     int first, len;
-    if (!packed_block(a.cu, a.nseq, a.total, blocks * kBlk, blockIdx.x / a.hv, err, &s->seq, &s->j, &first, &len)) return false;
+    if (!packed_block(a.cu, a.nseq, a.total, len_div, unit, err, &s->seq, &s->j, &first, &len)) return false;
     s->start = s->j * blocks * kBlk;
     if (s->j > 0 && s->start >= len) return false;
     s->seq_len = len;
@@ -150,8 +150,8 @@ struct SegCfg {
 
 template <int DK, int DV>
 __global__ void __launch_bounds__(kSegThreads, 1)
-linattn_segment_kernel(const __grid_constant__ LinattnMaps maps, const LinattnArgs a, int blocks,
-                       float4* __restrict__ states, int* err)
+linattn_segment_kernel(const __grid_constant__ LinattnMaps maps, const LinattnArgs a, int blocks, const Divisor seg_div,
+                       const Divisor hv_div, float4* __restrict__ states, int* err)
 {
     using L = SegCfg<DK, DV>;
     extern __shared__ uint8_t smem_raw[];
@@ -163,11 +163,11 @@ linattn_segment_kernel(const __grid_constant__ LinattnMaps maps, const LinattnAr
     volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L::kTm + 4);
     Powers* pw = reinterpret_cast<Powers*>(sm + L::kPow);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int h = blockIdx.x % a.hv;
+    const int unit = hv_div.d > 1 ? hv_div.div(blockIdx.x) : (int)blockIdx.x, h = blockIdx.x - unit * a.hv;
     griddep_launch_dependents();
     Segment sg;
     // the last segment of a sequence hands its state to no one
-    if (!this_segment(a, blocks, err, &sg) || sg.start + blocks * kBlk >= sg.seq_len) return;
+    if (!this_segment(a, blocks, seg_div, unit, err, &sg) || sg.start + blocks * kBlk >= sg.seq_len) return;
 
     if (tid == 0) {
         for (int s = 0; s < kSegStages; ++s) {
@@ -209,7 +209,7 @@ linattn_segment_kernel(const __grid_constant__ LinattnMaps maps, const LinattnAr
             }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
+        if (elect_one()) {
             bool ok = true;
             for (int n = 0; n < blocks * kPieces && ok; ++n) {
                 const int c = n / kPieces, p = n % kPieces;
@@ -292,8 +292,8 @@ struct OutCfg {
 
 template <int DK, int DV>
 __global__ void __launch_bounds__(kOutThreads, 1)
-linattn_output_kernel(const __grid_constant__ LinattnMaps maps, const LinattnArgs a, int blocks,
-                      const float4* __restrict__ states, int* err)
+linattn_output_kernel(const __grid_constant__ LinattnMaps maps, const LinattnArgs a, int blocks, const Divisor seg_div,
+                      const Divisor hv_div, const float4* __restrict__ states, int* err)
 {
     using L = OutCfg<DK, DV>;
     extern __shared__ uint8_t smem_raw[];
@@ -308,10 +308,10 @@ linattn_output_kernel(const __grid_constant__ LinattnMaps maps, const LinattnArg
     volatile int* bad_values = reinterpret_cast<volatile int*>(sm + L::kTm + 8);     // [4], by block mod 4
     Powers* pw = reinterpret_cast<Powers*>(sm + L::kPow);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int h = blockIdx.x % a.hv;
+    const int unit = hv_div.d > 1 ? hv_div.div(blockIdx.x) : (int)blockIdx.x, h = blockIdx.x - unit * a.hv;
     if (blockIdx.x == 0) check_offsets(a.cu, a.nseq, a.total, err);
     Segment sg;
-    if (!this_segment(a, blocks, err, &sg)) return;
+    if (!this_segment(a, blocks, seg_div, unit, err, &sg)) return;
     const int nb = (sg.len + kBlk - 1) / kBlk;             // 0 for an empty sequence
     const int last = sg.len - (nb - 1) * kBlk;             // tokens of the last block
     const bool ends = sg.start + sg.len >= sg.seq_len;     // this segment writes the final state
@@ -401,7 +401,7 @@ linattn_output_kernel(const __grid_constant__ LinattnMaps maps, const LinattnArg
         }
     } else if (warp == 1) {
         // ---------------------------------------------------------------- S = Q K^T, Yd = P V
-        if (lane == 0) {
+        if (elect_one()) {
             constexpr uint32_t idS = idesc_bf16_f32(128, kBlk, false, false), idY = idesc_bf16_f32(128, DV, false, true);
             bool ok = true;
             for (int c = 0; c < nb && ok; ++c) {
@@ -431,7 +431,7 @@ linattn_output_kernel(const __grid_constant__ LinattnMaps maps, const LinattnArg
         }
     } else if (warp == 2) {
         // ---------------------------------------------------------------- Yo = Q S
-        if (lane == 0) {
+        if (elect_one()) {
             constexpr uint32_t id = idesc_bf16_f32(128, DV, false, true);
             bool ok = true;
             for (int c = 0; c < nb && ok; ++c) {
@@ -451,7 +451,7 @@ linattn_output_kernel(const __grid_constant__ LinattnMaps maps, const LinattnArg
         }
     } else if (warp == 3) {
         // ---------------------------------------------------------------- U = K~^T V
-        if (lane == 0) {
+        if (elect_one()) {
             bool ok = true;
             int n = 0;
             for (int c = 0; c < nb && ok; ++c) {
@@ -726,17 +726,18 @@ cudaError_t launch_t(const LinattnArgs& a, float4* states, cudaStream_t s)
     const int blocks = segment_blocks(a.nseq, a.total, a.hv);
     const long long grid = (long long)packed_blocks(a.total, a.nseq, blocks * kBlk) * a.hv;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
+    const Divisor seg_div(blocks * kBlk), hv_div(a.hv);
     int* err = device_error_word();
     cudaError_t e = cudaSuccess;
     if (a.total > blocks * kBlk) {
         e = cudaFuncSetAttribute(linattn_segment_kernel<DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  SegCfg<DK, DV>::kBytes);
         if (e != cudaSuccess) return e;
-        linattn_segment_kernel<DK, DV><<<(unsigned)grid, kSegThreads, SegCfg<DK, DV>::kBytes, s>>>(maps, a, blocks, states, err);
+        linattn_segment_kernel<DK, DV><<<(unsigned)grid, kSegThreads, SegCfg<DK, DV>::kBytes, s>>>(maps, a, blocks, seg_div, hv_div, states, err);
     }
     e = cudaFuncSetAttribute(linattn_output_kernel<DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, OutCfg<DK, DV>::kBytes);
     if (e != cudaSuccess) return e;
-    linattn_output_kernel<DK, DV><<<(unsigned)grid, kOutThreads, OutCfg<DK, DV>::kBytes, s>>>(maps, a, blocks, states, err);
+    linattn_output_kernel<DK, DV><<<(unsigned)grid, kOutThreads, OutCfg<DK, DV>::kBytes, s>>>(maps, a, blocks, seg_div, hv_div, states, err);
     return cudaGetLastError();
 }
 

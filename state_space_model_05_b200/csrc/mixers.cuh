@@ -49,18 +49,27 @@ struct AttnDecodeArgs {
 // least one number, and there are at most total / Q + nseq of them.
 __host__ __device__ inline int packed_blocks(int total, int nseq, int Q) { return total / Q + nseq; }
 
+// a / d for 0 <= a < 2^31 and a divisor 2 <= d < 2^31 that the host knows: the kernels divide
+// offsets by block lengths before their first load, where a division's instructions are cold.
+struct Divisor {
+    int d;
+    unsigned long long inv;                          // floor(2^64 / d) + 1
+    explicit Divisor(int n) : d(n), inv(~0ULL / (unsigned long long)n + 1) {}
+    __device__ __forceinline__ int div(int a) const { return (int)__umul64hi((unsigned long long)(unsigned)a, inv); }
+};
+
 // Sequence, block within it, first token and sequence length of block number i, found by
 // whole warps (32 offsets per round of loads).  False (and SSD_ERR_SHAPE in the error word)
 // when the offsets around it are not a valid partition; a true return may still name a block
 // past its sequence's end (j * Q >= len).
-__device__ __forceinline__ bool packed_block(const int* __restrict__ cu, int nseq, int total, int Q, int i,
+__device__ __forceinline__ bool packed_block(const int* __restrict__ cu, int nseq, int total, const Divisor& Q, int i,
                                              int* err, int* seq, int* j, int* first, int* len)
 {
     const int lane = threadIdx.x & 31;
     int lo = 0, n = nseq;                            // the largest s with cu[s] / Q + s <= i is in [lo, lo + n)
     while (n > 1) {
         const int step = (n + 31) / 32, s = lo + lane * step;
-        const unsigned below = __ballot_sync(0xffffffffu, lane * step < n && cu[s] / Q + s <= i);
+        const unsigned below = __ballot_sync(0xffffffffu, lane * step < n && Q.div(max(cu[s], 0)) + s <= i);
         const int k = below ? 31 - __clz(below) : 0;
         lo += k * step;
         n = min(step, n - k * step);
@@ -71,7 +80,7 @@ __device__ __forceinline__ bool packed_block(const int* __restrict__ cu, int nse
         return false;
     }
     *seq = lo;
-    *j = i - (a / Q + lo);
+    *j = i - (Q.div(a) + lo);
     *first = a;
     *len = b - a;
     return *j >= 0;
