@@ -244,7 +244,7 @@ __device__ __noinline__ uint4 add_bad_values(const AttnArgs& a, uint4 out, int b
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-attn_prefill_tc_kernel(const __grid_constant__ AttnMaps maps, const AttnArgs a, int group, int span, const Divisor block_div,
+attn_prefill_tc_kernel(const __grid_constant__ AttnMaps maps, const __grid_constant__ AttnArgs a, int group, int span, const Divisor block_div,
                        const Divisor hkv_div, int* err)
 {
     using L = Cfg<D>;

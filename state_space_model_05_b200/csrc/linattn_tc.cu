@@ -34,89 +34,73 @@ namespace {
 
 constexpr int kBlk = 128;                                  // tokens per block
 constexpr int kHalf = kBlk * 128;                          // 64 dimensions of a block's rows
-constexpr int kPiece = 32;                                 // tokens of K~ formed at a time
-constexpr int kPieces = kBlk / kPiece;
-
-// Bytes of a 32-token piece of K~: three parts, each [dk / 64][32 rows][128 bytes].
-template <int DK> constexpr int kPartBytes = DK / 64 * kPiece * 128;
+constexpr int kConvThreads = 256;                          // threads that form K~
+// Tokens of K~ formed at a time: a 16-byte chunk per thread.
+template <int DK> constexpr int kPiece = kConvThreads * 8 / DK;
+template <int DK> constexpr int kPieces = kBlk / kPiece<DK>;
+constexpr int kPart = kConvThreads * 16;                   // bytes of one part of a piece: [dk / 64][tokens][128 bytes]
+constexpr int kSlot = 3 * kPart;
 
 // g^0 .. g^128 and, reversed, g^31 .. g^0
-struct Powers { float up[kBlk + 4]; float down[kPiece]; };
+constexpr int kSub = 32;
+struct Powers { float up[kBlk + 4]; float down[kSub]; };
 
 __device__ __forceinline__ void fill_powers(Powers* p, float ld, int tid, int threads)
 {
     for (int i = tid; i <= kBlk; i += threads) p->up[i] = decay_pow(ld, i);
-    for (int i = tid; i < kPiece; i += threads) p->down[i] = decay_pow(ld, kPiece - 1 - i);
+    for (int i = tid; i < kSub; i += threads) p->down[i] = decay_pow(ld, kSub - 1 - i);
 }
 
-// One 16-byte chunk (eight keys' elements of one token) times w, as three bf16 parts.
-__device__ __forceinline__ void split3(const uint4& k, float w, uint4 (&part)[3])
+// A thread's chunk (eight elements of one token) of piece p of a block's keys, times the token's
+// weight, as three bf16 parts: the product's 24 bits in three cuts of 8, so that the parts' sum
+// is exactly the fp32 product.  The swizzle permutes chunks within a row by the row's number mod
+// 8, which the piece keeps.  Rows from n on are zero whatever they hold.
+template <int DK>
+__device__ __forceinline__ void form_piece(uint4 (&part)[3], const uint8_t* keys, int p, int n, const float* up, float extra, int tid)
 {
+    constexpr int kRowChunks = kPiece<DK> * 8;             // chunks of a 64-dimension half
+    const int half = tid / kRowChunks, i = tid % kRowChunks, s = p * kPiece<DK> + (i >> 3);
+    const uint4 k = *reinterpret_cast<const uint4*>(keys + half * kHalf + p * kPiece<DK> * 128 + i * 16);
     const uint32_t in[4] = {k.x, k.y, k.z, k.w};
+    const float w = s < n ? up[n - 1 - s] * extra : 0.f;
     uint32_t out[3][4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        float a = bf16lo(in[j]) * w, b = bf16hi(in[j]) * w;
+        const uint32_t u = s < n ? in[j] : 0u;
+        float2 x = fmul2(make_float2(bf16lo(u), bf16hi(u)), make_float2(w, w));
 #pragma unroll
         for (int q = 0; q < 3; ++q) {
-            out[q][j] = pack_bf16x2(a, b);
-            a -= bf16lo(out[q][j]);
-            b -= bf16hi(out[q][j]);
+            const uint32_t a = __float_as_uint(x.x), b = __float_as_uint(x.y);
+            out[q][j] = __byte_perm(a, b, 0x7632);         // the upper halves of both
+            if (q < 2) x = ffma2(make_float2(__uint_as_float(a & 0xFFFF0000u), __uint_as_float(b & 0xFFFF0000u)), make_float2(-1.f, -1.f), x);
         }
     }
 #pragma unroll
     for (int q = 0; q < 3; ++q) part[q] = make_uint4(out[q][0], out[q][1], out[q][2], out[q][3]);
 }
 
-// A thread's chunks of piece p of a block's keys, weighted and split; the swizzle permutes
-// chunks within a row by the row's number mod 8, which the piece keeps.
-template <int DK, int kThreads>
-struct Convert {
-    static constexpr int kChunks = DK / 8 * kPiece / kThreads;
-    uint4 part[kChunks][3];
-    // w[s]: the weight of token s of the piece; rows from n on are zero whatever they hold
-    __device__ __forceinline__ void form(const uint8_t* keys, int p, int n, const float* up, float extra, int tid)
-    {
+__device__ __forceinline__ void write_piece(uint8_t* slot, const uint4 (&part)[3], int tid)
+{
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c) {
-            const int i = tid + c * kThreads, half = i / (kPiece * 8), r = (i >> 3) % kPiece, s = p * kPiece + r;
-            const uint4 k = *reinterpret_cast<const uint4*>(keys + half * kHalf + p * kPiece * 128 + (i % (kPiece * 8)) * 16);
-            if (s < n) {
-                split3(k, up[n - 1 - s] * extra, part[c]);
-            } else {
-#pragma unroll
-                for (int q = 0; q < 3; ++q) part[c][q] = make_uint4(0u, 0u, 0u, 0u);
-            }
-        }
-    }
-    __device__ __forceinline__ void write(uint8_t* dst, int tid) const
-    {
-#pragma unroll
-        for (int c = 0; c < kChunks; ++c) {
-            const int i = tid + c * kThreads;
-#pragma unroll
-            for (int q = 0; q < 3; ++q) *reinterpret_cast<uint4*>(dst + q * kPartBytes<DK> + i * 16) = part[c][q];
-        }
-    }
-};
+    for (int q = 0; q < 3; ++q) *reinterpret_cast<uint4*>(slot + q * kPart + tid * 16) = part[q];
+}
 
-// The products of one piece: U (+)= K~^T V over its 32 tokens.
+// The products of one piece: U (+)= K~^T V over its tokens.
 template <int DK, int DV>
 __device__ __forceinline__ void issue_state(uint32_t tU, uint32_t conv, uint32_t values, int p, bool fresh)
 {
     constexpr uint32_t id = idesc_bf16_f32(128, DV, true, true);
-    const uint64_t dV = smem_desc_sw128(values + p * kPiece * 128, kHalf, 1024);
+    const uint64_t dV = smem_desc_sw128(values + p * kPiece<DK> * 128, kHalf, 1024);
+    // (dk = 64: rows 64 .. 127 of the product, from what lies behind, are never read)
+    const uint64_t dK = smem_desc_sw128(conv, kPiece<DK> * 128, 1024);
 #pragma unroll
-    for (int q = 0; q < 3; ++q) {
-        // dk = 64: rows 64 .. 127 of the product are never read
-        const uint64_t dK = smem_desc_sw128(conv + q * kPartBytes<DK>, kPiece * 128, 1024);
+    for (int q = 0; q < 3; ++q)
 #pragma unroll
-        for (int ks = 0; ks < kPiece / 16; ++ks)
-            umma_f16(tU, desc_advance(dK, ks * 2048), desc_advance(dV, ks * 2048), id, (fresh && q == 0 && ks == 0) ? 0u : 1u);
-    }
+        for (int ks = 0; ks < kPiece<DK> / 16; ++ks)
+            umma_f16(tU, desc_advance(dK, q * kPart + ks * 2048), desc_advance(dV, ks * 2048), id, (fresh && q == 0 && ks == 0) ? 0u : 1u);
 }
 
-struct LinattnMaps { CUtensorMap q, k, v; };
+struct LinattnMaps { CUtensorMap q, k, v, out; };
 
 // The segment of this CTA: sequence, segment within it, its first token and number of tokens.
 struct Segment { int seq, j, first, start, len, seq_len; };
@@ -134,14 +118,14 @@ __device__ __forceinline__ bool this_segment(const LinattnArgs& a, int blocks, c
 }
 
 // ================================================================ a segment's own state
-constexpr int kSegThreads = 384, kSegConv = 256, kSegStages = 2, kSegSlots = 2;
+constexpr int kSegThreads = 128 + kConvThreads, kSegStages = 2, kSegSlots = 4;
 
 template <int DK, int DV>
 struct SegCfg {
     static constexpr int kKeys = DK / 64 * kHalf, kValues = DV / 64 * kHalf;
     static constexpr int kStage = kKeys + kValues;
     static constexpr int kConv = kSegStages * kStage;
-    static constexpr int kPow = kConv + kSegSlots * 3 * kPartBytes<DK> + 4096;   // (rows past dk = 64 are read)
+    static constexpr int kPow = kConv + kSegSlots * kSlot + (DK == 64 ? kPart : 0);
     static constexpr int kBar = (kPow + (int)sizeof(Powers) + 7) / 8 * 8;
     static constexpr int kTm = kBar + (2 * kSegStages + 2 * kSegSlots + 1) * 8;
     static constexpr int kBytes = kTm + 16 + 1024;
@@ -150,7 +134,7 @@ struct SegCfg {
 
 template <int DK, int DV>
 __global__ void __launch_bounds__(kSegThreads, 1)
-linattn_segment_kernel(const __grid_constant__ LinattnMaps maps, const LinattnArgs a, int blocks, const Divisor seg_div,
+linattn_segment_kernel(const __grid_constant__ LinattnMaps maps, const __grid_constant__ LinattnArgs a, int blocks, const Divisor seg_div,
                        const Divisor hv_div, float4* __restrict__ states, int* err)
 {
     using L = SegCfg<DK, DV>;
@@ -175,7 +159,7 @@ linattn_segment_kernel(const __grid_constant__ LinattnMaps maps, const LinattnAr
             mbar_init(&empty[s], 1);
         }
         for (int s = 0; s < kSegSlots; ++s) {
-            mbar_init(&conv_full[s], kSegConv);
+            mbar_init(&conv_full[s], kConvThreads / 32);
             mbar_init(&conv_empty[s], 1);
         }
         mbar_init(done, 1);
@@ -193,7 +177,7 @@ linattn_segment_kernel(const __grid_constant__ LinattnMaps maps, const LinattnAr
     tc_fence_after();
     const uint32_t tmem = *tslot;
     auto wait = [&](uint64_t* bar, int phase) { return mbar_wait_or_abort(bar, phase & 1, err, abort_flag); };
-    auto conv = [&](int n) { return sm + L::kConv + (n % kSegSlots) * 3 * kPartBytes<DK>; };
+    auto conv = [&](int n) { return sm + L::kConv + (n % kSegSlots) * kSlot; };
 
     if (warp == 0) {
         if (lane == 0) {
@@ -211,14 +195,14 @@ linattn_segment_kernel(const __grid_constant__ LinattnMaps maps, const LinattnAr
     } else if (warp == 1) {
         if (elect_one()) {
             bool ok = true;
-            for (int n = 0; n < blocks * kPieces && ok; ++n) {
-                const int c = n / kPieces, p = n % kPieces;
+            for (int n = 0; n < blocks * kPieces<DK> && ok; ++n) {
+                const int c = n / kPieces<DK>, p = n % kPieces<DK>;
                 ok = wait(&conv_full[n % kSegSlots], n / kSegSlots);
                 if (!ok) break;
                 tc_fence_after();
                 issue_state<DK, DV>(tmem, smem_u32(conv(n)), smem_u32(sm + (c % kSegStages) * L::kStage + L::kKeys), p, n == 0);
                 umma_commit(&conv_empty[n % kSegSlots]);
-                if (p == kPieces - 1) umma_commit(&empty[c % kSegStages]);
+                if (p == kPieces<DK> - 1) umma_commit(&empty[c % kSegStages]);
             }
             umma_commit(done);
             wait(done, 0);                                 // no TMEM is released with products in flight
@@ -227,18 +211,19 @@ linattn_segment_kernel(const __grid_constant__ LinattnMaps maps, const LinattnAr
         const int ctid = tid - 128;
         bool ok = true;
         for (int c = 0; c < blocks && ok; ++c) {
-            ok = wait(&full[c % kSegStages], c / kSegStages);
+            ok = __all_sync(0xffffffffu, wait(&full[c % kSegStages], c / kSegStages));
             // weights from the segment's end: the products accumulate over all its blocks
             const float extra = decay_pow(ld, (blocks - 1 - c) * kBlk);
-            for (int p = 0; p < kPieces && ok; ++p) {
-                const int n = c * kPieces + p;
-                Convert<DK, kSegConv> x;
-                x.form(sm + (c % kSegStages) * L::kStage, p, kBlk, pw->up, extra, ctid);
-                ok = n < kSegSlots || wait(&conv_empty[n % kSegSlots], n / kSegSlots - 1);
+            for (int p = 0; p < kPieces<DK>; ++p) {
+                const int n = c * kPieces<DK> + p;
+                uint4 part[3];
+                form_piece<DK>(part, sm + (c % kSegStages) * L::kStage, p, kBlk, pw->up, extra, ctid);
+                ok = ok && (n < kSegSlots || __all_sync(0xffffffffu, wait(&conv_empty[n % kSegSlots], n / kSegSlots - 1)));
                 if (!ok) break;
-                x.write(conv(n), ctid);
+                write_piece(conv(n), part, ctid);
                 fence_proxy_async_smem();
-                mbar_arrive(&conv_full[n % kSegSlots]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&conv_full[n % kSegSlots]);
             }
         }
         if (__all_sync(0xffffffffu, ok && wait(done, 0))) {
@@ -270,9 +255,9 @@ linattn_segment_kernel(const __grid_constant__ LinattnMaps maps, const LinattnAr
 }
 
 // ================================================================ outputs and final states
-constexpr int kOutThreads = 640;                           // TMA, 3 MMA, 4 conversion, 8 state, 4 output warps
-constexpr int kConvThreads = 128;
-constexpr int kWarpConv = 4, kWarpState = 8, kWarpOut = 16;
+constexpr int kOutThreads = 768;                           // TMA, 3 MMA, 8 conversion, 8 state, 4 output warps
+constexpr int kWarpConv = 4, kWarpState = 12, kWarpOut = 20;
+constexpr int kConvSlots = 2;
 
 template <int DK, int DV>
 struct OutCfg {
@@ -281,7 +266,7 @@ struct OutCfg {
     static constexpr int kQSlots = DK + DV <= 192 ? 2 : 1;
     static constexpr int kK = kQSlots * kKeys, kV = kK + 2 * kKeys, kImg = kV + 2 * kValues;
     static constexpr int kConv = kImg + kImage;
-    static constexpr int kPow = kConv + 3 * kPartBytes<DK> + (DK == 64 ? 4096 : 0);
+    static constexpr int kPow = kConv + kConvSlots * kSlot + (DK == 64 ? kPart : 0);   // (read behind the last slot)
     static constexpr int kBar = (kPow + (int)sizeof(Powers) + 7) / 8 * 8;
     static constexpr int kTm = kBar + 32 * 8;
     static constexpr int kBytes = kTm + 32 + 1024;
@@ -290,9 +275,28 @@ struct OutCfg {
     static constexpr uint32_t kS = 0, kYd = 128, kYo = 256, kU = 384;
 };
 
+// One output of a row from the row's own sum over its block, which holds a value that is not
+// finite: only the rows from that token on see it (the product's zeros would not hide it).
+__device__ __noinline__ float own_sum(const LinattnArgs& a, const Powers* pw, size_t base, int r, int h, int col)
+{
+    const size_t hq = (size_t)(h / (a.hv / a.hq)) * a.dk;
+    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + (base + r) * a.q_stride + hq;
+    float y = 0.f;
+#pragma unroll 1
+    for (int s = 0; s <= r; ++s) {
+        const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(a.k) + (base + s) * a.k_stride + hq;
+        float p = 0.f;
+#pragma unroll 1
+        for (int d = 0; d < a.dk; ++d) p = fmaf(__bfloat162float(q[d]), __bfloat162float(k[d]), p);
+        y = fmaf(p * pw->up[r - s],
+                 __bfloat162float(static_cast<const __nv_bfloat16*>(a.v)[(base + s) * a.v_stride + (size_t)h * a.dv + col]), y);
+    }
+    return y;
+}
+
 template <int DK, int DV>
 __global__ void __launch_bounds__(kOutThreads, 1)
-linattn_output_kernel(const __grid_constant__ LinattnMaps maps, const LinattnArgs a, int blocks, const Divisor seg_div,
+linattn_output_kernel(const __grid_constant__ LinattnMaps maps, const __grid_constant__ LinattnArgs a, int blocks, const Divisor seg_div,
                       const Divisor hv_div, const float4* __restrict__ states, int* err)
 {
     using L = OutCfg<DK, DV>;
@@ -302,7 +306,7 @@ linattn_output_kernel(const __grid_constant__ LinattnMaps maps, const LinattnArg
     uint64_t *q_full = bars, *q_empty = bars + 2, *k_full = bars + 4, *k_empty = bars + 6, *v_full = bars + 8,
              *v_empty = bars + 10, *v_ok = bars + 12, *s_full = bars + 14, *p_full = bars + 15, *yd_full = bars + 16,
              *yd_free = bars + 17, *yo_full = bars + 18, *yo_free = bars + 19, *img_full = bars + 20, *u_full = bars + 21,
-             *u_free = bars + 22, *conv_full = bars + 23, *conv_empty = bars + 24;
+             *u_free = bars + 22, *conv_full = bars + 23, *conv_empty = bars + 25;
     uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + L::kTm);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L::kTm + 4);
     volatile int* bad_values = reinterpret_cast<volatile int*>(sm + L::kTm + 8);     // [4], by block mod 4
@@ -323,7 +327,7 @@ linattn_output_kernel(const __grid_constant__ LinattnMaps maps, const LinattnArg
             mbar_init(&k_full[s], 1);
             mbar_init(&k_empty[s], 1 + kConvThreads / 32);
             mbar_init(&v_full[s], 1);
-            mbar_init(&v_empty[s], 2);
+            mbar_init(&v_empty[s], 1);
             mbar_init(&v_ok[s], kConvThreads / 32);
         }
         mbar_init(s_full, 1);
@@ -335,8 +339,10 @@ linattn_output_kernel(const __grid_constant__ LinattnMaps maps, const LinattnArg
         mbar_init(img_full, 8);
         mbar_init(u_full, 1);
         mbar_init(u_free, 8);
-        mbar_init(conv_full, kConvThreads / 32);
-        mbar_init(conv_empty, 1);
+        for (int s = 0; s < kConvSlots; ++s) {
+            mbar_init(&conv_full[s], kConvThreads / 32);
+            mbar_init(&conv_empty[s], 1);
+        }
         *abort_flag = 0;
         for (int i = 0; i < 4; ++i) bad_values[i] = 0;
         fence_mbar_init();
@@ -359,44 +365,34 @@ linattn_output_kernel(const __grid_constant__ LinattnMaps maps, const LinattnArg
     auto tokens = [&](int c) { return c == nb - 1 ? last : kBlk; };
     constexpr int QS = L::kQSlots;
 
+    // registers by role, together the 768 x 80 that the CTA was launched with
+    if (warp < kWarpConv) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     if (warp == 0) {
         // ---------------------------------------------------------------- loads
-        if (lane == 0) {
+        if (elect_one()) {
             const int hq = h / (a.hv / a.hq);
-            // two streams, polled: a block's keys and values, and its queries, whose slot is free
-            // earlier or later than theirs
-            int kv = 0, cq = 0;
-            uint32_t idle = 0;
-            while (kv < nb || cq < nb) {
-                bool moved = false;
-                if (kv < nb && (kv < 2 || (mbar_test_wait(&k_empty[kv & 1], (kv / 2 - 1) & 1) &&
-                                           mbar_test_wait(&v_empty[kv & 1], (kv / 2 - 1) & 1)))) {
-                    const int row = sg.first + kv * kBlk, s = kv & 1;
-                    mbar_expect_tx(&k_full[s], L::kKeys);
-                    for (int x = 0; x < DK; x += 64) tma_load_3d(kslot(kv) + x / 64 * kHalf, &maps.k, x, hq, row, &k_full[s]);
-                    mbar_expect_tx(&v_full[s], L::kValues);
-                    for (int x = 0; x < DV; x += 64) tma_load_3d(vslot(kv) + x / 64 * kHalf, &maps.v, x, h, row, &v_full[s]);
-                    if (kv > cq)                           // queries that wait for their slot wait in the L2
-                        for (int x = 0; x < DK; x += 64) tma_prefetch_3d(&maps.q, x, hq, row);
-                    ++kv;
-                    moved = true;
-                }
-                if (cq < nb && (cq < QS || mbar_test_wait(&q_empty[cq % QS], (cq / QS - 1) & 1))) {
-                    mbar_expect_tx(&q_full[cq % QS], L::kKeys);
-                    for (int x = 0; x < DK; x += 64)
-                        tma_load_3d(qslot(cq) + x / 64 * kHalf, &maps.q, x, hq, sg.first + cq * kBlk, &q_full[cq % QS]);
-                    ++cq;
-                    moved = true;
-                }
-                if (moved) {
-                    idle = 0;
-                } else if (++idle >= (1u << 24)) {
-                    record_error(err, SSD_ERR_TIMEOUT);
-                    *abort_flag = 1;
-                    break;
-                } else if ((idle & 1023u) == 0 && *abort_flag) {
-                    break;
-                }
+            auto load_kv = [&](int c) {
+                const int row = sg.first + c * kBlk, s = c & 1;
+                mbar_expect_tx(&k_full[s], L::kKeys);
+                for (int x = 0; x < DK; x += 64) tma_load_3d(kslot(c) + x / 64 * kHalf, &maps.k, x, hq, row, &k_full[s]);
+                mbar_expect_tx(&v_full[s], L::kValues);
+                for (int x = 0; x < DV; x += 64) tma_load_3d(vslot(c) + x / 64 * kHalf, &maps.v, x, h, row, &v_full[s]);
+                if (c >= QS)                               // queries that wait for their slot wait in the L2
+                    for (int x = 0; x < DK; x += 64) tma_prefetch_3d(&maps.q, x, hq, row);
+            };
+            // a block's queries replace the block before's once its scores and carried part are formed,
+            // which is before that block's keys and values make room for the next one's
+            if (nb > 0) load_kv(0);
+#pragma unroll 1
+            for (int c = 0; c < nb; ++c) {
+                if (c >= QS && !wait(&q_empty[c % QS], c / QS - 1)) break;
+                mbar_expect_tx(&q_full[c % QS], L::kKeys);
+                for (int x = 0; x < DK; x += 64)
+                    tma_load_3d(qslot(c) + x / 64 * kHalf, &maps.q, x, hq, sg.first + c * kBlk, &q_full[c % QS]);
+                if (c + 1 == nb) break;
+                if (c >= 1 && !(wait(&k_empty[(c + 1) & 1], (c + 1) / 2 - 1) && wait(&v_empty[(c + 1) & 1], (c + 1) / 2 - 1))) break;
+                load_kv(c + 1);
             }
         }
     } else if (warp == 1) {
@@ -424,7 +420,6 @@ linattn_output_kernel(const __grid_constant__ LinattnMaps maps, const LinattnArg
 #pragma unroll
                 for (int ks = 0; ks < kBlk / 16; ++ks)
                     umma_f16_ts(tmem + L::kYd, tmem + L::kS + ks * 8, desc_advance(dV, ks * 2048), idY, ks > 0 ? 1u : 0u);
-                umma_commit(&v_empty[c & 1]);
                 umma_commit(yd_full);
             }
             if (ok && nb > 0) wait(yd_full, nb - 1);       // no TMEM is released with products in flight
@@ -455,22 +450,24 @@ linattn_output_kernel(const __grid_constant__ LinattnMaps maps, const LinattnArg
             bool ok = true;
             int n = 0;
             for (int c = 0; c < nb && ok; ++c) {
-                const int pieces = (tokens(c) + kPiece - 1) / kPiece;
+                const int pieces = (tokens(c) + kPiece<DK> - 1) / kPiece<DK>;
+#pragma unroll 1
                 for (int p = 0; p < pieces; ++p, ++n) {
-                    ok = wait(conv_full, n) && (p > 0 || c == 0 || wait(u_free, c - 1));
+                    ok = wait(&conv_full[n % kConvSlots], n / kConvSlots) && (p > 0 || c == 0 || wait(u_free, c - 1));
                     if (!ok) break;
                     tc_fence_after();
-                    issue_state<DK, DV>(tmem + L::kU, smem_u32(sm + L::kConv), smem_u32(vslot(c)), p, p == 0);
-                    umma_commit(conv_empty);
+                    issue_state<DK, DV>(tmem + L::kU, smem_u32(sm + L::kConv + (n % kConvSlots) * kSlot), smem_u32(vslot(c)), p, p == 0);
+                    umma_commit(&conv_empty[n % kConvSlots]);
                 }
                 if (!ok) break;
-                umma_commit(&v_empty[c & 1]);
                 umma_commit(u_full);
             }
             if (ok && nb > 0) wait(u_full, nb - 1);
         }
+    }
     } else if (warp < kWarpState) {
         // ---------------------------------------------------------------- values checked, K~ formed
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         const int ctid = tid - kWarpConv * 32;
         const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
         bool ok = true;
@@ -481,7 +478,7 @@ linattn_output_kernel(const __grid_constant__ LinattnMaps maps, const LinattnArg
             if (!ok) break;
             // rows behind the sequence's end are another's: zeroed, since 0 x inf is not 0.  Values
             // that are not finite are left to the output warps, as P's zeros would not hide them.
-            __nv_bfloat162 acc = zero;
+            __nv_bfloat162 acc[4] = {zero, zero, zero, zero};
 #pragma unroll 4
             for (int i = ctid; i < kBlk * DV / 8; i += kConvThreads) {
                 uint4* p = reinterpret_cast<uint4*>(vslot(c)) + i;
@@ -491,28 +488,31 @@ linattn_output_kernel(const __grid_constant__ LinattnMaps maps, const LinattnArg
                     const uint4 u = *p;
                     const __nv_bfloat162* x = reinterpret_cast<const __nv_bfloat162*>(&u);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) acc = __hfma2(x[e], zero, acc);
+                    for (int e = 0; e < 4; ++e) acc[e] = __hfma2(x[e], zero, acc[e]);
                 }
             }
-            if (__hisnan(acc.x) || __hisnan(acc.y)) bad_values[c & 3] = c + 1;
+            const __nv_bfloat162 all = __hadd2(__hadd2(acc[0], acc[1]), __hadd2(acc[2], acc[3]));
+            if (__hisnan(all.x) || __hisnan(all.y)) bad_values[c & 3] = c + 1;
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&v_ok[c & 1]);
             ok = wait_warp(&k_full[c & 1], c / 2);
-            for (int p = 0; p < (rows + kPiece - 1) / kPiece && ok; ++p, ++n) {
-                Convert<DK, kConvThreads> x;
-                x.form(kslot(c), p, rows, pw->up, 1.f, ctid);
-                ok = n == 0 || wait_warp(conv_empty, n - 1);
+#pragma unroll 1
+            for (int p = 0; p < (rows + kPiece<DK> - 1) / kPiece<DK> && ok; ++p, ++n) {
+                uint4 part[3];
+                form_piece<DK>(part, kslot(c), p, rows, pw->up, 1.f, ctid);
+                ok = n < kConvSlots || wait_warp(&conv_empty[n % kConvSlots], n / kConvSlots - 1);
                 if (!ok) break;
-                x.write(sm + L::kConv, ctid);
+                write_piece(sm + L::kConv + (n % kConvSlots) * kSlot, part, ctid);
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(conv_full);
+                if (lane == 0) mbar_arrive(&conv_full[n % kConvSlots]);
             }
             if (lane == 0) mbar_arrive(&k_empty[c & 1]);
         }
     } else if (warp < kWarpOut) {
         // ---------------------------------------------------------------- the carried state
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
         constexpr int NC = DV / 2;                         // columns per thread
         const int quarter = warp & 3, row = quarter * 32 + lane, c0 = ((warp - kWarpState) >> 2) * NC;
         const bool mine = row < a.dk;
@@ -586,11 +586,13 @@ linattn_output_kernel(const __grid_constant__ LinattnMaps maps, const LinattnArg
         }
     } else {
         // ---------------------------------------------------------------- P, and the outputs
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");
         const int quarter = warp & 3, r = quarter * 32 + lane;
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
         const float g_out = pw->up[r + 1];
+        const bool leader = warp == kWarpOut && lane == 0;
         for (int c = 0; c < nb; ++c) {
-            if (!wait_warp(s_full, c)) break;
+            bool ok = wait_warp(s_full, c);
             tc_fence_after();
 #pragma unroll
             for (int kc = 0; kc < 4; ++kc) {
@@ -626,55 +628,75 @@ linattn_output_kernel(const __grid_constant__ LinattnMaps maps, const LinattnArg
             tmem_wait_st();
             tc_fence_before();
             mbar_arrive(p_full);
-            if (!wait_warp(yd_full, c) || !wait_warp(yo_full, c)) break;
+            if (leader && c > 0) {                         // the last block's values may be replaced once its outputs are read
+                bulk_wait_group_read0();
+                mbar_arrive(&v_empty[(c - 1) & 1]);
+            }
+            // (after the block's state product, too, its values are not needed any more)
+            ok = ok && wait_warp(yd_full, c) && wait_warp(yo_full, c) && wait_warp(u_full, c);
             tc_fence_after();
-            const int t = c * kBlk + r;                    // token within the segment
-            const bool live = t < sg.len;
             const bool bad = bad_values[c & 3] == c + 1;
-            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + ((size_t)(sg.first + t) * a.hv + h) * a.dv;
-#pragma unroll
-            for (int q = 0; q < DV / 16; ++q) {
-                uint32_t yd[16], yo[16];
-                tmem_ld16(tmem + lanes + L::kYd + 16 * q, yd);
-                tmem_ld16(tmem + lanes + L::kYo + 16 * q, yo);
+            const int rows = sg.len - c * kBlk;            // rows from here on belong to another sequence
+            const size_t base = sg.first + (size_t)c * kBlk;
+            // the outputs go over the block's values, in the layout that they were loaded in
+            uint8_t* stage = vslot(c) + r * 128;
+#pragma unroll 1
+            for (int q = 0; q < DV / 32; ++q) {
+                uint32_t yd[32], yo[32];
+                tmem_ld32(tmem + lanes + L::kYd + 32 * q, yd);
+                tmem_ld32(tmem + lanes + L::kYo + 32 * q, yo);
                 tmem_wait_ld();
-                float y[16];
-                if (bad && live) {
-                    // the block holds a value that is not finite: the row's own sum, so that only
-                    // the rows from that token on see it
-                    const size_t base = sg.first + (size_t)c * kBlk, hq = (size_t)(h / (a.hv / a.hq)) * a.dk;
-                    const __nv_bfloat16* qr = static_cast<const __nv_bfloat16*>(a.q) + (base + r) * a.q_stride + hq;
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) y[e] = 0.f;
-                    for (int s = 0; s <= r; ++s) {
-                        const __nv_bfloat16* kr = static_cast<const __nv_bfloat16*>(a.k) + (base + s) * a.k_stride + hq;
-                        const __nv_bfloat16* vr = static_cast<const __nv_bfloat16*>(a.v) + (base + s) * a.v_stride + (size_t)h * a.dv;
-                        float p = 0.f;
-                        for (int d = 0; d < a.dk; ++d) p = fmaf(__bfloat162float(qr[d]), __bfloat162float(kr[d]), p);
-                        p *= pw->up[r - s];
+                for (int e = 0; e < 32; e += 8) {
+                    uint32_t o[4];
 #pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            if (16 * q + e < a.dv) y[e] = fmaf(p, __bfloat162float(vr[16 * q + e]), y[e]);
+                    for (int z = 0; z < 4; ++z) {
+                        const float2 y = fmul2(ffma2(make_float2(g_out, g_out),
+                                                     make_float2(__uint_as_float(yo[e + 2 * z]), __uint_as_float(yo[e + 2 * z + 1])),
+                                                     make_float2(__uint_as_float(yd[e + 2 * z]), __uint_as_float(yd[e + 2 * z + 1]))),
+                                               make_float2(a.scale, a.scale));
+                        o[z] = pack_bf16x2(y.x, y.y);
                     }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) y[e] = __uint_as_float(yd[e]);
+                    *reinterpret_cast<uint4*>(stage + (q >> 1) * kHalf + ((((q & 1) * 4 + e / 8) ^ (r & 7)) << 4)) =
+                        make_uint4(o[0], o[1], o[2], o[3]);
                 }
-#pragma unroll
-                for (int e = 0; e < 16; ++e) y[e] = a.scale * fmaf(g_out, __uint_as_float(yo[e]), y[e]);
-                if (live) {
-#pragma unroll
-                    for (int e = 0; e < 16; e += 8)
-                        if (16 * q + e < a.dv)
-                            *reinterpret_cast<uint4*>(out + 16 * q + e) =
-                                make_uint4(pack_bf16x2(y[e], y[e + 1]), pack_bf16x2(y[e + 2], y[e + 3]),
-                                           pack_bf16x2(y[e + 4], y[e + 5]), pack_bf16x2(y[e + 6], y[e + 7]));
+                if (bad) {
+                    // (rare: the staged row again, a column at a time)
+#pragma unroll 1
+                    for (int e = 0; e < 32; ++e) {
+                        uint32_t carried;
+                        tmem_ld1(tmem + lanes + L::kYo + 32 * q + e, carried);
+                        tmem_wait_ld();
+                        if (r < rows && 32 * q + e < a.dv)
+                            *reinterpret_cast<__nv_bfloat16*>(stage + (q >> 1) * kHalf + ((((q & 1) * 4 + (e >> 3)) ^ (r & 7)) << 4) + 2 * (e & 7)) =
+                                __float2bfloat16_rn(a.scale * fmaf(g_out, __uint_as_float(carried), own_sum(a, pw, base, r, h, 32 * q + e)));
+                    }
                 }
             }
             tc_fence_before();
             mbar_arrive(yd_free);
             mbar_arrive(yo_free);
+            fence_proxy_async_smem();
+            if (!named_bar_and(1, 128, ok)) break;         // all four warps have staged theirs, or all stop
+            if (rows >= kBlk) {
+                if (leader) {
+                    for (int x = 0; x < DV; x += 64) tma_store_3d(&maps.out, x, h, (int)base, vslot(c) + x / 64 * kHalf);
+                    bulk_commit_group();
+                }
+            } else {
+                // the sequence's last rows: whole rows at a time
+                constexpr int kChunks = DV / 8;
+                const int ch = lane % kChunks;
+#pragma unroll 2
+                for (int k = 0; k < kChunks; ++k) {
+                    const int row = quarter * 32 + k * (32 / kChunks) + lane / kChunks;
+                    const uint4 v = *reinterpret_cast<const uint4*>(vslot(c) + (ch >> 3) * kHalf + row * 128 + (((ch & 7) ^ (row & 7)) << 4));
+                    if (row < rows && 8 * ch < a.dv)
+                        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + ((base + row) * a.hv + h) * a.dv + 8 * ch) = v;
+                }
+            }
         }
+        if (leader) bulk_wait_group0();
     }
     tc_fence_before();
     __syncthreads();
@@ -721,7 +743,8 @@ cudaError_t launch_t(const LinattnArgs& a, float4* states, cudaStream_t s)
     LinattnMaps maps = {};
     if (a.total > 0 && (!token_map(&maps.q, a.q, a.dk, a.hq, a.total, a.q_stride) ||
                         !token_map(&maps.k, a.k, a.dk, a.hq, a.total, a.k_stride) ||
-                        !token_map(&maps.v, a.v, a.dv, a.hv, a.total, a.v_stride)))
+                        !token_map(&maps.v, a.v, a.dv, a.hv, a.total, a.v_stride) ||
+                        !token_map(&maps.out, a.out, a.dv, a.hv, a.total, (long long)a.hv * a.dv)))
         return cudaErrorInvalidValue;
     const int blocks = segment_blocks(a.nseq, a.total, a.hv);
     const long long grid = (long long)packed_blocks(a.total, a.nseq, blocks * kBlk) * a.hv;
