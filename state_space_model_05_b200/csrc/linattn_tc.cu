@@ -5,7 +5,7 @@
 //
 // in blocks of n <= 128 tokens with the carried state S (dk x dv) at the block's start:
 //     o_t = scale (sum_{s<=t} g^(t-s) (q_t.k_s) v_s + g^(t+1) S^T q_t)
-//     S  <- g^n S + sum_s (g^(n-1-s) k_s) v_s^T
+//     S  <- g^n S + sum_s k_s (g^(n-1-s) v_s)^T
 // The decay does not depend on the tokens, so every factor comes from one table g^0 .. g^128.
 //
 // linattn_output_kernel: one CTA walks the blocks of one (segment, value head), the state in
@@ -16,10 +16,9 @@
 // buys segments for all SMs; the host picks the length (segment_blocks).
 //
 // Per block: S = Q K^T, masked and decayed into P (bf16, over S in TMEM), Yd = P V; Yo = Q S from
-// the state's bf16 image; U = K~^T V with K~ = g^(n-1-s) k_s.  K~ is carried as the sum of three
+// the state's bf16 image; U = K^T V~ with V~ = g^(n-1-s) v_s.  V~ is carried as the sum of three
 // bf16 numbers (24 bits), so that the state keeps fp32 accuracy; P and the state's image are
-// rounded to bf16 once, each by at most half the output's own rounding step.  The four
-// products take less time than the block's loads, so their number does not show.
+// rounded to bf16 once, each by at most half the output's own rounding step.
 #include <cuda.h>
 
 #include "mixers.cuh"
@@ -34,11 +33,11 @@ namespace {
 
 constexpr int kBlk = 128;                                  // tokens per block
 constexpr int kHalf = kBlk * 128;                          // 64 dimensions of a block's rows
-constexpr int kConvThreads = 256;                          // threads that form K~
-// Tokens of K~ formed at a time: a 16-byte chunk per thread.
-template <int DK> constexpr int kPiece = kConvThreads * 8 / DK;
-template <int DK> constexpr int kPieces = kBlk / kPiece<DK>;
-constexpr int kPart = kConvThreads * 16;                   // bytes of one part of a piece: [dk / 64][tokens][128 bytes]
+constexpr int kConvThreads = 256;                          // threads that form a piece of V~
+// Tokens of V~ formed at a time: a 16-byte chunk per thread.
+template <int DV> constexpr int kPiece = kConvThreads * 8 / DV;
+template <int DV> constexpr int kPieces = kBlk / kPiece<DV>;
+constexpr int kPart = kConvThreads * 16;                   // bytes of one part of a piece: [dv / 64][tokens][128 bytes]
 constexpr int kSlot = 3 * kPart;
 
 // g^0 .. g^128 and, reversed, g^31 .. g^0
@@ -51,23 +50,15 @@ __device__ __forceinline__ void fill_powers(Powers* p, float ld, int tid, int th
     for (int i = tid; i < kSub; i += threads) p->down[i] = decay_pow(ld, kSub - 1 - i);
 }
 
-// A thread's chunk (eight elements of one token) of piece p of a block's keys, times the token's
-// weight, as three bf16 parts: the product's 24 bits in three cuts of 8, so that the parts' sum
-// is exactly the fp32 product.  The swizzle permutes chunks within a row by the row's number mod
-// 8, which the piece keeps.  Rows from n on are zero whatever they hold.
-template <int DK>
-__device__ __forceinline__ void form_piece(uint4 (&part)[3], const uint8_t* keys, int p, int n, const float* up, float extra, int tid)
+// A thread's chunk (eight elements of one token, s) of a piece of V, times w, as three bf16 parts:
+// the product's 24 bits in three cuts of 8, so that the parts' sum is exactly the fp32 product.
+__device__ __forceinline__ void split3(uint4 (&part)[3], const uint4& v, float w)
 {
-    constexpr int kRowChunks = kPiece<DK> * 8;             // chunks of a 64-dimension half
-    const int half = tid / kRowChunks, i = tid % kRowChunks, s = p * kPiece<DK> + (i >> 3);
-    const uint4 k = *reinterpret_cast<const uint4*>(keys + half * kHalf + p * kPiece<DK> * 128 + i * 16);
-    const uint32_t in[4] = {k.x, k.y, k.z, k.w};
-    const float w = s < n ? up[n - 1 - s] * extra : 0.f;
+    const uint32_t in[4] = {v.x, v.y, v.z, v.w};
     uint32_t out[3][4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const uint32_t u = s < n ? in[j] : 0u;
-        float2 x = fmul2(make_float2(bf16lo(u), bf16hi(u)), make_float2(w, w));
+        float2 x = fmul2(make_float2(bf16lo(in[j]), bf16hi(in[j])), make_float2(w, w));
 #pragma unroll
         for (int q = 0; q < 3; ++q) {
             const uint32_t a = __float_as_uint(x.x), b = __float_as_uint(x.y);
@@ -79,25 +70,36 @@ __device__ __forceinline__ void form_piece(uint4 (&part)[3], const uint8_t* keys
     for (int q = 0; q < 3; ++q) part[q] = make_uint4(out[q][0], out[q][1], out[q][2], out[q][3]);
 }
 
+// Where a thread's chunk of piece p lies in a block's tile (the swizzle permutes chunks within a
+// row by the row's number mod 8, which the piece keeps), and the chunk's token.
+template <int DV>
+__device__ __forceinline__ uint4* piece_chunk(uint8_t* values, int p, int tid, int* token)
+{
+    constexpr int kRowChunks = kPiece<DV> * 8;             // chunks of a 64-dimension half
+    const int half = tid / kRowChunks, i = tid % kRowChunks;
+    *token = p * kPiece<DV> + (i >> 3);
+    return reinterpret_cast<uint4*>(values + half * kHalf + p * kPiece<DV> * 128 + i * 16);
+}
+
 __device__ __forceinline__ void write_piece(uint8_t* slot, const uint4 (&part)[3], int tid)
 {
 #pragma unroll
     for (int q = 0; q < 3; ++q) *reinterpret_cast<uint4*>(slot + q * kPart + tid * 16) = part[q];
 }
 
-// The products of one piece: U (+)= K~^T V over its tokens.
+// The products of one piece: U (+)= K^T V~ over its tokens.
 template <int DK, int DV>
-__device__ __forceinline__ void issue_state(uint32_t tU, uint32_t conv, uint32_t values, int p, bool fresh)
+__device__ __forceinline__ void issue_state(uint32_t tU, uint32_t keys, uint32_t conv, int p, bool fresh)
 {
     constexpr uint32_t id = idesc_bf16_f32(128, DV, true, true);
-    const uint64_t dV = smem_desc_sw128(values + p * kPiece<DK> * 128, kHalf, 1024);
-    // (dk = 64: rows 64 .. 127 of the product, from what lies behind, are never read)
-    const uint64_t dK = smem_desc_sw128(conv, kPiece<DK> * 128, 1024);
+    // (dk = 64: rows 64 .. 127 of the product, from what lies behind the keys, are never read)
+    const uint64_t dK = smem_desc_sw128(keys + p * kPiece<DV> * 128, kHalf, 1024);
+    const uint64_t dV = smem_desc_sw128(conv, kPiece<DV> * 128, 1024);
 #pragma unroll
     for (int q = 0; q < 3; ++q)
 #pragma unroll
-        for (int ks = 0; ks < kPiece<DK> / 16; ++ks)
-            umma_f16(tU, desc_advance(dK, q * kPart + ks * 2048), desc_advance(dV, ks * 2048), id, (fresh && q == 0 && ks == 0) ? 0u : 1u);
+        for (int ks = 0; ks < kPiece<DV> / 16; ++ks)
+            umma_f16(tU, desc_advance(dK, ks * 2048), desc_advance(dV, q * kPart + ks * 2048), id, (fresh && q == 0 && ks == 0) ? 0u : 1u);
 }
 
 struct LinattnMaps { CUtensorMap q, k, v, out; };
@@ -125,7 +127,7 @@ struct SegCfg {
     static constexpr int kKeys = DK / 64 * kHalf, kValues = DV / 64 * kHalf;
     static constexpr int kStage = kKeys + kValues;
     static constexpr int kConv = kSegStages * kStage;
-    static constexpr int kPow = kConv + kSegSlots * kSlot + (DK == 64 ? kPart : 0);
+    static constexpr int kPow = kConv + kSegSlots * kSlot;
     static constexpr int kBar = (kPow + (int)sizeof(Powers) + 7) / 8 * 8;
     static constexpr int kTm = kBar + (2 * kSegStages + 2 * kSegSlots + 1) * 8;
     static constexpr int kBytes = kTm + 16 + 1024;
@@ -195,14 +197,14 @@ linattn_segment_kernel(const __grid_constant__ LinattnMaps maps, const __grid_co
     } else if (warp == 1) {
         if (elect_one()) {
             bool ok = true;
-            for (int n = 0; n < blocks * kPieces<DK> && ok; ++n) {
-                const int c = n / kPieces<DK>, p = n % kPieces<DK>;
+            for (int n = 0; n < blocks * kPieces<DV> && ok; ++n) {
+                const int c = n / kPieces<DV>, p = n % kPieces<DV>;
                 ok = wait(&conv_full[n % kSegSlots], n / kSegSlots);
                 if (!ok) break;
                 tc_fence_after();
-                issue_state<DK, DV>(tmem, smem_u32(conv(n)), smem_u32(sm + (c % kSegStages) * L::kStage + L::kKeys), p, n == 0);
+                issue_state<DK, DV>(tmem, smem_u32(sm + (c % kSegStages) * L::kStage), smem_u32(conv(n)), p, n == 0);
                 umma_commit(&conv_empty[n % kSegSlots]);
-                if (p == kPieces<DK> - 1) umma_commit(&empty[c % kSegStages]);
+                if (p == kPieces<DV> - 1) umma_commit(&empty[c % kSegStages]);
             }
             umma_commit(done);
             wait(done, 0);                                 // no TMEM is released with products in flight
@@ -214,10 +216,13 @@ linattn_segment_kernel(const __grid_constant__ LinattnMaps maps, const __grid_co
             ok = __all_sync(0xffffffffu, wait(&full[c % kSegStages], c / kSegStages));
             // weights from the segment's end: the products accumulate over all its blocks
             const float extra = decay_pow(ld, (blocks - 1 - c) * kBlk);
-            for (int p = 0; p < kPieces<DK>; ++p) {
-                const int n = c * kPieces<DK> + p;
+#pragma unroll 2
+            for (int p = 0; p < kPieces<DV>; ++p) {
+                const int n = c * kPieces<DV> + p;
+                int t;
                 uint4 part[3];
-                form_piece<DK>(part, sm + (c % kSegStages) * L::kStage, p, kBlk, pw->up, extra, ctid);
+                const uint4 v = *piece_chunk<DV>(sm + (c % kSegStages) * L::kStage + L::kKeys, p, ctid, &t);
+                split3(part, v, pw->up[kBlk - 1 - t] * extra);
                 ok = ok && (n < kSegSlots || __all_sync(0xffffffffu, wait(&conv_empty[n % kSegSlots], n / kSegSlots - 1)));
                 if (!ok) break;
                 write_piece(conv(n), part, ctid);
@@ -255,7 +260,7 @@ linattn_segment_kernel(const __grid_constant__ LinattnMaps maps, const __grid_co
 }
 
 // ================================================================ outputs and final states
-constexpr int kOutThreads = 768;                           // TMA, 3 MMA, 8 conversion, 8 state, 4 output warps
+constexpr int kOutThreads = 768;                           // TMA, 3 MMA, 8 + 8 for V~ (the latter for the state, too), 4 output warps
 constexpr int kWarpConv = 4, kWarpState = 12, kWarpOut = 20;
 constexpr int kConvSlots = 2;
 
@@ -266,7 +271,7 @@ struct OutCfg {
     static constexpr int kQSlots = DK + DV <= 192 ? 2 : 1;
     static constexpr int kK = kQSlots * kKeys, kV = kK + 2 * kKeys, kImg = kV + 2 * kValues;
     static constexpr int kConv = kImg + kImage;
-    static constexpr int kPow = kConv + kConvSlots * kSlot + (DK == 64 ? kPart : 0);   // (read behind the last slot)
+    static constexpr int kPow = kConv + kConvSlots * kSlot;
     static constexpr int kBar = (kPow + (int)sizeof(Powers) + 7) / 8 * 8;
     static constexpr int kTm = kBar + 32 * 8;
     static constexpr int kBytes = kTm + 32 + 1024;
@@ -306,7 +311,7 @@ linattn_output_kernel(const __grid_constant__ LinattnMaps maps, const __grid_con
     uint64_t *q_full = bars, *q_empty = bars + 2, *k_full = bars + 4, *k_empty = bars + 6, *v_full = bars + 8,
              *v_empty = bars + 10, *v_ok = bars + 12, *s_full = bars + 14, *p_full = bars + 15, *yd_full = bars + 16,
              *yd_free = bars + 17, *yo_full = bars + 18, *yo_free = bars + 19, *img_full = bars + 20, *u_full = bars + 21,
-             *u_free = bars + 22, *conv_full = bars + 23, *conv_empty = bars + 25;
+             *u_free = bars + 22, *conv_full = bars + 23, *conv_empty = bars + 25, *v_used = bars + 27;
     uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + L::kTm);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L::kTm + 4);
     volatile int* bad_values = reinterpret_cast<volatile int*>(sm + L::kTm + 8);     // [4], by block mod 4
@@ -325,10 +330,11 @@ linattn_output_kernel(const __grid_constant__ LinattnMaps maps, const __grid_con
             mbar_init(&q_full[s], 1);
             mbar_init(&q_empty[s], 2);
             mbar_init(&k_full[s], 1);
-            mbar_init(&k_empty[s], 1 + kConvThreads / 32);
+            mbar_init(&k_empty[s], 2);
             mbar_init(&v_full[s], 1);
             mbar_init(&v_empty[s], 1);
-            mbar_init(&v_ok[s], kConvThreads / 32);
+            mbar_init(&v_ok[s], 2 * kConvThreads / 32);
+            mbar_init(&v_used[s], 1);
         }
         mbar_init(s_full, 1);
         mbar_init(p_full, 128);
@@ -364,6 +370,52 @@ linattn_output_kernel(const __grid_constant__ LinattnMaps maps, const __grid_con
     auto vslot = [&](int c) { return sm + L::kV + (c & 1) * L::kValues; };
     auto tokens = [&](int c) { return c == nb - 1 ? last : kBlk; };
     constexpr int QS = L::kQSlots;
+    // The pieces of block c's V~ whose number is `odd` mod 2, formed by 256 threads.  On the way the
+    // values themselves are looked after: rows behind the sequence's end are another's and zeroed,
+    // since 0 x inf is not 0; values that are not finite are left to the output warps, as P's zeros
+    // would not hide them.
+    auto weighted_values = [&](int c, int odd, int gt) {
+        const int rows = tokens(c);
+        if (!wait_warp(&v_full[c & 1], c / 2)) return false;
+        const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
+        __nv_bfloat162 acc[4] = {zero, zero, zero, zero};  // NaN as soon as one of its values is not finite
+        uint8_t* slot = sm + L::kConv + odd * kSlot;
+#pragma unroll 1
+        for (int p = odd; p < kPieces<DV>; p += 2) {
+            int t;
+            uint4* at = piece_chunk<DV>(vslot(c), p, gt, &t);
+            uint4 v = *at, part[3];
+            if (t >= rows) {
+                v = make_uint4(0u, 0u, 0u, 0u);
+                *at = v;
+            }
+            if (p * kPiece<DV> >= rows) continue;          // (the same for all threads)
+            const __nv_bfloat162* x = reinterpret_cast<const __nv_bfloat162*>(&v);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[e] = __hfma2(x[e], zero, acc[e]);
+            split3(part, v, t < rows ? pw->up[rows - 1 - t] : 0.f);
+            const int use = c * (kPieces<DV> / 2) + p / 2;
+            if (use > 0 && !wait_warp(&conv_empty[odd], use - 1)) return false;
+            write_piece(slot, part, gt);
+            const int cut = (p + 1) * kPiece<DV> - rows;   // the piece's keys behind the sequence's end, zeroed alike
+            if (cut > 0) {
+                if (!wait_warp(&k_full[c & 1], c / 2)) return false;
+                for (int i = gt; i < cut * (DK / 8); i += kConvThreads) {
+                    const int ch = i % (DK / 8), row = rows + i / (DK / 8);
+                    *reinterpret_cast<uint4*>(kslot(c) + (ch >> 3) * kHalf + row * 128 + (ch & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&conv_full[odd]);
+        }
+        const __nv_bfloat162 all = __hadd2(__hadd2(acc[0], acc[1]), __hadd2(acc[2], acc[3]));
+        if (__hisnan(all.x) || __hisnan(all.y)) bad_values[c & 3] = c + 1;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&v_ok[c & 1]);
+        return true;
+    };
 
     // registers by role, together the 768 x 80 that the CTA was launched with
     if (warp < kWarpConv) {
@@ -405,7 +457,7 @@ linattn_output_kernel(const __grid_constant__ LinattnMaps maps, const __grid_con
                 if (!ok) break;
                 tc_fence_after();
                 const uint64_t dQ = smem_desc_sw128(smem_u32(qslot(c)), 16, 1024), dK = smem_desc_sw128(smem_u32(kslot(c)), 16, 1024);
-#pragma unroll
+#pragma unroll 1
                 for (int ks = 0; ks < DK / 16; ++ks) {
                     const uint32_t off = (ks >> 2) * kHalf + (ks & 3) * 32;
                     umma_f16(tmem + L::kS, desc_advance(dQ, off), desc_advance(dK, off), idS, ks > 0 ? 1u : 0u);
@@ -417,7 +469,7 @@ linattn_output_kernel(const __grid_constant__ LinattnMaps maps, const __grid_con
                 if (!ok) break;
                 tc_fence_after();
                 const uint64_t dV = smem_desc_sw128(smem_u32(vslot(c)), kHalf, 1024);
-#pragma unroll
+#pragma unroll 1
                 for (int ks = 0; ks < kBlk / 16; ++ks)
                     umma_f16_ts(tmem + L::kYd, tmem + L::kS + ks * 8, desc_advance(dV, ks * 2048), idY, ks > 0 ? 1u : 0u);
                 umma_commit(yd_full);
@@ -435,7 +487,7 @@ linattn_output_kernel(const __grid_constant__ LinattnMaps maps, const __grid_con
                 tc_fence_after();
                 const uint64_t dQ = smem_desc_sw128(smem_u32(qslot(c)), 16, 1024);
                 const uint64_t dS = smem_desc_sw128(smem_u32(sm + L::kImg), DK * 128, 1024);
-#pragma unroll
+#pragma unroll 1
                 for (int ks = 0; ks < DK / 16; ++ks)
                     umma_f16(tmem + L::kYo, desc_advance(dQ, (ks >> 2) * kHalf + (ks & 3) * 32), desc_advance(dS, ks * 2048), id,
                              ks > 0 ? 1u : 0u);
@@ -448,70 +500,32 @@ linattn_output_kernel(const __grid_constant__ LinattnMaps maps, const __grid_con
         // ---------------------------------------------------------------- U = K~^T V
         if (elect_one()) {
             bool ok = true;
-            int n = 0;
             for (int c = 0; c < nb && ok; ++c) {
-                const int pieces = (tokens(c) + kPiece<DK> - 1) / kPiece<DK>;
+                const int pieces = (tokens(c) + kPiece<DV> - 1) / kPiece<DV>;
+                ok = wait(&k_full[c & 1], c / 2);
 #pragma unroll 1
-                for (int p = 0; p < pieces; ++p, ++n) {
-                    ok = wait(&conv_full[n % kConvSlots], n / kConvSlots) && (p > 0 || c == 0 || wait(u_free, c - 1));
+                for (int p = 0; p < pieces; ++p) {         // piece p comes through slot p mod 2
+                    ok = ok && wait(&conv_full[p & 1], c * (kPieces<DV> / 2) + p / 2) && (p > 0 || c == 0 || wait(u_free, c - 1));
                     if (!ok) break;
                     tc_fence_after();
-                    issue_state<DK, DV>(tmem + L::kU, smem_u32(sm + L::kConv + (n % kConvSlots) * kSlot), smem_u32(vslot(c)), p, p == 0);
-                    umma_commit(&conv_empty[n % kConvSlots]);
+                    issue_state<DK, DV>(tmem + L::kU, smem_u32(kslot(c)), smem_u32(sm + L::kConv + (p & 1) * kSlot), p, p == 0);
+                    umma_commit(&conv_empty[p & 1]);
                 }
                 if (!ok) break;
+                umma_commit(&k_empty[c & 1]);
+                umma_commit(&v_used[c & 1]);
                 umma_commit(u_full);
             }
             if (ok && nb > 0) wait(u_full, nb - 1);
         }
     }
     } else if (warp < kWarpState) {
-        // ---------------------------------------------------------------- values checked, K~ formed
+        // ---------------------------------------------------------------- V~, even pieces
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-        const int ctid = tid - kWarpConv * 32;
-        const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
-        bool ok = true;
-        int n = 0;
-        for (int c = 0; c < nb && ok; ++c) {
-            const int rows = tokens(c);
-            ok = wait_warp(&v_full[c & 1], c / 2);
-            if (!ok) break;
-            // rows behind the sequence's end are another's: zeroed, since 0 x inf is not 0.  Values
-            // that are not finite are left to the output warps, as P's zeros would not hide them.
-            __nv_bfloat162 acc[4] = {zero, zero, zero, zero};
-#pragma unroll 4
-            for (int i = ctid; i < kBlk * DV / 8; i += kConvThreads) {
-                uint4* p = reinterpret_cast<uint4*>(vslot(c)) + i;
-                if ((i >> 3) % kBlk >= rows) {
-                    *p = make_uint4(0u, 0u, 0u, 0u);
-                } else {
-                    const uint4 u = *p;
-                    const __nv_bfloat162* x = reinterpret_cast<const __nv_bfloat162*>(&u);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[e] = __hfma2(x[e], zero, acc[e]);
-                }
-            }
-            const __nv_bfloat162 all = __hadd2(__hadd2(acc[0], acc[1]), __hadd2(acc[2], acc[3]));
-            if (__hisnan(all.x) || __hisnan(all.y)) bad_values[c & 3] = c + 1;
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&v_ok[c & 1]);
-            ok = wait_warp(&k_full[c & 1], c / 2);
-#pragma unroll 1
-            for (int p = 0; p < (rows + kPiece<DK> - 1) / kPiece<DK> && ok; ++p, ++n) {
-                uint4 part[3];
-                form_piece<DK>(part, kslot(c), p, rows, pw->up, 1.f, ctid);
-                ok = n < kConvSlots || wait_warp(&conv_empty[n % kConvSlots], n / kConvSlots - 1);
-                if (!ok) break;
-                write_piece(sm + L::kConv + (n % kConvSlots) * kSlot, part, ctid);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&conv_full[n % kConvSlots]);
-            }
-            if (lane == 0) mbar_arrive(&k_empty[c & 1]);
-        }
+        for (int c = 0; c < nb; ++c)
+            if (!weighted_values(c, 0, tid - kWarpConv * 32)) break;
     } else if (warp < kWarpOut) {
-        // ---------------------------------------------------------------- the carried state
+        // ---------------------------------------------------------------- V~, odd pieces; the carried state
         asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
         constexpr int NC = DV / 2;                         // columns per thread
         const int quarter = warp & 3, row = quarter * 32 + lane, c0 = ((warp - kWarpState) >> 2) * NC;
@@ -557,7 +571,7 @@ linattn_output_kernel(const __grid_constant__ LinattnMaps maps, const __grid_con
         if (nb > 0) write_image();
         bool ok = true;
         for (int c = 0; c < nb; ++c) {
-            ok = wait_warp(u_full, c);
+            ok = weighted_values(c, 1, tid - kWarpState * 32) && wait_warp(u_full, c);
             if (!ok) break;
             tc_fence_after();
             const float g = pw->up[tokens(c)];
@@ -594,7 +608,7 @@ linattn_output_kernel(const __grid_constant__ LinattnMaps maps, const __grid_con
         for (int c = 0; c < nb; ++c) {
             bool ok = wait_warp(s_full, c);
             tc_fence_after();
-#pragma unroll
+#pragma unroll 1
             for (int kc = 0; kc < 4; ++kc) {
                 uint32_t pk[16];
                 if (kc <= quarter) {                       // the same for the warp's 32 rows
@@ -632,8 +646,9 @@ linattn_output_kernel(const __grid_constant__ LinattnMaps maps, const __grid_con
                 bulk_wait_group_read0();
                 mbar_arrive(&v_empty[(c - 1) & 1]);
             }
-            // (after the block's state product, too, its values are not needed any more)
-            ok = ok && wait_warp(yd_full, c) && wait_warp(yo_full, c) && wait_warp(u_full, c);
+            // (after the block's state product, too, its values are not needed any more: a barrier
+            // per value slot says so, as u_full may be a block further on by now)
+            ok = ok && wait_warp(yd_full, c) && wait_warp(yo_full, c) && wait_warp(&v_used[c & 1], c / 2);
             tc_fence_after();
             const bool bad = bad_values[c & 3] == c + 1;
             const int rows = sg.len - c * kBlk;            // rows from here on belong to another sequence
