@@ -120,7 +120,7 @@ __device__ __forceinline__ bool this_segment(const LinattnArgs& a, int blocks, c
 }
 
 // ================================================================ a segment's own state
-constexpr int kSegThreads = 128 + kConvThreads, kSegStages = 2, kSegSlots = 4;
+constexpr int kSegThreads = 128 + 2 * kConvThreads, kSegStages = 2, kSegSlots = 4;   // two groups take turns at the pieces
 
 template <int DK, int DV>
 struct SegCfg {
@@ -210,14 +210,14 @@ linattn_segment_kernel(const __grid_constant__ LinattnMaps maps, const __grid_co
             wait(done, 0);                                 // no TMEM is released with products in flight
         }
     } else if (warp >= 4) {
-        const int ctid = tid - 128;
+        const int group = (tid - 128) / kConvThreads, ctid = (tid - 128) % kConvThreads;
         bool ok = true;
         for (int c = 0; c < blocks && ok; ++c) {
             ok = __all_sync(0xffffffffu, wait(&full[c % kSegStages], c / kSegStages));
             // weights from the segment's end: the products accumulate over all its blocks
             const float extra = decay_pow(ld, (blocks - 1 - c) * kBlk);
-#pragma unroll 2
-            for (int p = 0; p < kPieces<DV>; ++p) {
+#pragma unroll 1
+            for (int p = group; p < kPieces<DV>; p += 2) {
                 const int n = c * kPieces<DV> + p;
                 int t;
                 uint4 part[3];
@@ -234,10 +234,10 @@ linattn_segment_kernel(const __grid_constant__ LinattnMaps maps, const __grid_co
         if (__all_sync(0xffffffffu, ok && wait(done, 0))) {
             tc_fence_after();
             // quads of columns as [column quad][row]: consecutive lanes write consecutive quads
-            const int row = (warp & 3) * 32 + lane, c0 = ((warp - 4) >> 2) * (DV / 2);
+            const int row = (warp & 3) * 32 + lane, c0 = ((warp - 4) >> 2) * (DV / 4);
             float4* dst = states + (size_t)blockIdx.x * (DK * DV / 4);
 #pragma unroll
-            for (int q = 0; q < DV / 32; ++q) {
+            for (int q = 0; q < DV / 64; ++q) {
                 uint32_t v[16];
                 tmem_ld16(tmem + ((uint32_t)((warp & 3) * 32) << 16) + c0 + 16 * q, v);
                 tmem_wait_ld();
