@@ -201,7 +201,7 @@ attn_decode_bf16_kernel(const __grid_constant__ CacheMaps maps, const AttnDecode
     const long long x0 = W * c / G, x1 = W * (c + 1) / G;
     Cursor cur;
     cur.start(a.lens, a.capacity, at, x0, un.per_row);
-    auto wait = [&](uint64_t* bar, int phase) { return mbar_wait_or_abort(bar, phase & 1, err, abort_flag); };
+    auto wait = [&](uint64_t* bar, int phase) { return mbar_wait_compact(bar, phase & 1, err, abort_flag); };
 
     if (warp == kWarps) {
         if (lane == 0) {

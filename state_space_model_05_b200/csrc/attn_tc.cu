@@ -304,8 +304,8 @@ attn_prefill_tc_kernel(const __grid_constant__ AttnMaps maps, const __grid_const
         if (to_fix) mbar_arrive(slot);
     };
     const uint32_t tmem = *tslot;
-    auto wait = [&](uint64_t* bar, int phase) { return mbar_wait_or_abort(bar, phase & 1, err, abort_flag); };
-    auto poll = [&](uint64_t* bar, int phase) { return mbar_poll_or_abort(bar, phase & 1, err, abort_flag); };
+    auto wait = [&](uint64_t* bar, int phase) { return mbar_wait_compact(bar, phase & 1, err, abort_flag); };
+    auto poll = [&](uint64_t* bar, int phase) { return mbar_wait_compact<true>(bar, phase & 1, err, abort_flag); };
 
     // the softmax threads hold a row of scores each: 216 registers for them, 72 for the other
     // warps (together the 384 x 168 that the CTA was launched with)

@@ -178,7 +178,7 @@ linattn_segment_kernel(const __grid_constant__ LinattnMaps maps, const __grid_co
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tslot;
-    auto wait = [&](uint64_t* bar, int phase) { return mbar_wait_or_abort(bar, phase & 1, err, abort_flag); };
+    auto wait = [&](uint64_t* bar, int phase) { return mbar_wait_compact(bar, phase & 1, err, abort_flag); };
     auto conv = [&](int n) { return sm + L::kConv + (n % kSegSlots) * kSlot; };
 
     if (warp == 0) {
@@ -363,7 +363,7 @@ linattn_output_kernel(const __grid_constant__ LinattnMaps maps, const __grid_con
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tslot;
-    auto wait = [&](uint64_t* bar, int phase) { return mbar_wait_or_abort(bar, phase & 1, err, abort_flag); };
+    auto wait = [&](uint64_t* bar, int phase) { return mbar_wait_compact(bar, phase & 1, err, abort_flag); };
     auto wait_warp = [&](uint64_t* bar, int phase) { return (bool)__all_sync(0xffffffffu, wait(bar, phase)); };
     auto qslot = [&](int c) { return sm + (c % L::kQSlots) * L::kKeys; };
     auto kslot = [&](int c) { return sm + L::kK + (c & 1) * L::kKeys; };

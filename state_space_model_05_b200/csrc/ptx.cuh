@@ -77,15 +77,20 @@ __device__ __forceinline__ bool mbar_wait_or_abort(uint64_t* bar, uint32_t parit
     return false;
 }
 
-// The same wait polled with the non-blocking test, for threads whose waits are short and on
-// the critical path.
-__device__ __forceinline__ bool mbar_poll_or_abort(uint64_t* bar, uint32_t parity, int* err,
-                                                   volatile int* abort) {
-    for (uint32_t i = 0; i < (1u << 26); ++i) {
-        if (mbar_test_wait(bar, parity)) return true;
-        if ((i & 1023u) == 1023u && *abort) return false;
-    }
-    record_error(err, SSD_ERR_TIMEOUT);
+// The same wait in few instructions, for kernels whose warps run so much different code that it
+// crowds the instruction cache.  kPoll: with the non-blocking test, for threads whose waits are
+// short and on the critical path.
+template <bool kPoll = false>
+__device__ __forceinline__ bool mbar_wait_compact(uint64_t* bar, uint32_t parity, int* err, volatile int* abort) {
+    uint32_t i = 0;
+    bool done;
+#pragma unroll 1
+    do {
+        done = kPoll ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity);
+        if (done) return true;
+        ++i;
+    } while (i < (kPoll ? 1u << 26 : 1u << 22) && ((i & 1023u) || !*abort));
+    if (!*abort) record_error(err, SSD_ERR_TIMEOUT);
     *abort = 1;
     return false;
 }
@@ -303,6 +308,13 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
         ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
           "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]),
           "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+// 32 lanes x 8 consecutive 32-bit columns from registers.
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+        ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
         : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() {
