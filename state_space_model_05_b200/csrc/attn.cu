@@ -7,6 +7,7 @@
 // running maximum m and sum of each row (one pass); exponentials are taken in base 2, with
 // log2(e) folded into the scale.
 #include "mixers.cuh"
+#include "ptx.cuh"
 
 namespace ssd {
 
@@ -17,62 +18,73 @@ constexpr float kLog2e = 1.44269504088896341f;
 __device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
 
 // ================================================================ packed prompts, CUDA cores
-// A CTA takes 64 queries of one head and walks the keys up to its diagonal, 64 at a time.
-constexpr int kTok = 64;
-constexpr int kThreads = 256;
-constexpr int kLd = kMixMaxDim + 4;
-constexpr int kLdP = kTok + 4;
+// A CTA takes 32 queries of one head and walks the keys up to its diagonal, 64 at a time: small
+// enough that a few hundred tokens fill the GPU and four CTAs share an SM, which hides the loads
+// of one behind the products of another.  Products run on packed fp32 pairs: the scores' over
+// pairs of dimensions, the outputs' over pairs of columns.
+constexpr int kRows = 32;
+constexpr int kKeys = 64;
+constexpr int kThreads = 128;
+constexpr int kLdP = kKeys + 4;
 
-template <typename T>
+// `rows` rows of `cols` elements (a multiple of 4) as fp32 into padded shared rows, zeros past
+// them.  (Rows of D + 4 floats: 16-byte reads of 8 rows hit 8 different bank quads.)
+template <typename T, int D, int kCount>
 __device__ __forceinline__ void load_rows(float* dst, const T* src, long long stride, int rows, int cols, float mul)
 {
-    for (int i = threadIdx.x; i < kTok * (kMixMaxDim / 4); i += kThreads) {
-        const int r = i / (kMixMaxDim / 4), c = 4 * (i % (kMixMaxDim / 4));
+#pragma unroll 8
+    for (int i = threadIdx.x; i < kCount * (D / 4); i += kThreads) {
+        const int r = i / (D / 4), c = 4 * (i % (D / 4));
         float4 x = (r < rows && c < cols) ? load4<T>(src + (size_t)r * stride + c) : make_float4(0.f, 0.f, 0.f, 0.f);
         x.x *= mul; x.y *= mul; x.z *= mul; x.w *= mul;
-        *reinterpret_cast<float4*>(dst + r * kLd + c) = x;
+        *reinterpret_cast<float4*>(dst + r * (D + 4) + c) = x;
     }
 }
 
-__device__ __forceinline__ void fma4(float4& a, float s, const float4& b)
-{
-    a.x = fmaf(s, b.x, a.x); a.y = fmaf(s, b.y, a.y); a.z = fmaf(s, b.z, a.z); a.w = fmaf(s, b.w, a.w);
-}
+__device__ __forceinline__ float2 lo2(const float4& x) { return make_float2(x.x, x.y); }
+__device__ __forceinline__ float2 hi2(const float4& x) { return make_float2(x.z, x.w); }
 
-template <typename T>
+template <typename T, int D>
 __global__ void __launch_bounds__(kThreads)
 attn_prefill_kernel(const AttnArgs a, const Divisor block, int* err)
 {
+    constexpr int kLd = D + 4, kCols = D / 64;             // output columns per thread: 4 kCols
     extern __shared__ float sm[];
-    float *sq = sm, *sk = sq + kTok * kLd, *sv = sk + kTok * kLd, *sp = sv + kTok * kLd;
+    float *sq = sm, *sk = sq + kRows * kLd, *sv = sk + kKeys * kLd, *sp = sv + kKeys * kLd;
     const int h = blockIdx.y, tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     if (blockIdx.x == 0 && h == 0) check_offsets(a.cu, a.nseq, a.total, err);
     int seq, j, first, len;
     // the blocks with the most keys first
     if (!packed_block(a.cu, a.nseq, a.total, block, gridDim.x - 1 - blockIdx.x, err, &seq, &j, &first, &len)) return;
-    const int n = min(kTok, len - j * kTok);
+    const int q0 = j * kRows, n = min(kRows, len - q0);
     if (n <= 0) return;
-    const size_t t0 = (size_t)first + (size_t)j * kTok;
-    const int hk = h / (a.hq / a.hkv);
-    load_rows<T>(sq, static_cast<const T*>(a.q) + t0 * a.q_stride + (size_t)h * a.dim, a.q_stride, n, a.dim,
-                 a.scale * kLog2e);
+    const size_t t0 = (size_t)first + q0;
+    const int hk = h / (a.hq / a.hkv), tiles = (q0 + n - 1) / kKeys + 1;
+    load_rows<T, D, kRows>(sq, static_cast<const T*>(a.q) + t0 * a.q_stride + (size_t)h * a.dim, a.q_stride, n, a.dim,
+                           a.scale * kLog2e);
     // thread: rows 4 ty + i, score columns tx + 16 jj, output columns 4 tx .. + 3 (and 64 more)
     float m[4], l[4];
-    float4 acc[4][2];
+    float2 acc[4][kCols][2];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         m[i] = neg_inf();
         l[i] = 0.f;
-        acc[i][0] = acc[i][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) acc[i][c][0] = acc[i][c][1] = make_float2(0.f, 0.f);
     }
-    for (int kb = 0; kb <= j; ++kb) {
-        const size_t s0 = (size_t)first + (size_t)kb * kTok;
-        const int ns = min(kTok, len - kb * kTok);
+    for (int kb = 0; kb < tiles; ++kb) {
+        const size_t s0 = (size_t)first + (size_t)kb * kKeys;
+        const int ns = min(kKeys, len - kb * kKeys);
         __syncthreads();
-        load_rows<T>(sk, static_cast<const T*>(a.k) + s0 * a.k_stride + (size_t)hk * a.dim, a.k_stride, ns, a.dim, 1.f);
-        load_rows<T>(sv, static_cast<const T*>(a.v) + s0 * a.v_stride + (size_t)hk * a.dim, a.v_stride, ns, a.dim, 1.f);
+        load_rows<T, D, kKeys>(sk, static_cast<const T*>(a.k) + s0 * a.k_stride + (size_t)hk * a.dim, a.k_stride, ns, a.dim, 1.f);
+        load_rows<T, D, kKeys>(sv, static_cast<const T*>(a.v) + s0 * a.v_stride + (size_t)hk * a.dim, a.v_stride, ns, a.dim, 1.f);
         __syncthreads();
-        float p[4][4] = {};
+        float2 p2[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int jj = 0; jj < 4; ++jj) p2[i][jj] = make_float2(0.f, 0.f);
+#pragma unroll 2
         for (int d = 0; d < a.dim; d += 4) {
             float4 x[4], y[4];
 #pragma unroll
@@ -83,16 +95,17 @@ attn_prefill_kernel(const AttnArgs a, const Divisor block, int* err)
             for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int jj = 0; jj < 4; ++jj)
-                    p[i][jj] = fmaf(x[i].x, y[jj].x, fmaf(x[i].y, y[jj].y, fmaf(x[i].z, y[jj].z, fmaf(x[i].w, y[jj].w, p[i][jj]))));
+                    p2[i][jj] = ptx::ffma2(hi2(x[i]), hi2(y[jj]), ptx::ffma2(lo2(x[i]), lo2(y[jj]), p2[i][jj]));
         }
+        const int diag = q0 - kb * kKeys;                  // key s is seen from row t on: s <= t + diag
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int t = 4 * ty + i;
-            float top = m[i];
+            float p[4], top = m[i];
 #pragma unroll
             for (int jj = 0; jj < 4; ++jj) {
-                if (kb == j && tx + 16 * jj > t) p[i][jj] = neg_inf();
-                top = fmaxf(top, p[i][jj]);
+                p[jj] = tx + 16 * jj <= t + diag ? p2[i][jj].x + p2[i][jj].y : neg_inf();
+                top = fmaxf(top, p[jj]);
             }
 #pragma unroll
             for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -102,27 +115,51 @@ attn_prefill_kernel(const AttnArgs a, const Divisor block, int* err)
             float sum = 0.f;
 #pragma unroll
             for (int jj = 0; jj < 4; ++jj) {
-                const float x = exp2f(p[i][jj] - base);
+                const float x = exp2f(p[jj] - base);
                 sum += x;
                 sp[t * kLdP + tx + 16 * jj] = x;
             }
             l[i] = fmaf(l[i], keep, sum);
 #pragma unroll
-            for (int jj = 0; jj < 2; ++jj) {
-                acc[i][jj].x *= keep; acc[i][jj].y *= keep; acc[i][jj].z *= keep; acc[i][jj].w *= keep;
+            for (int c = 0; c < kCols; ++c) {
+                acc[i][c][0] = ptx::fmul2(acc[i][c][0], make_float2(keep, keep));
+                acc[i][c][1] = ptx::fmul2(acc[i][c][1], make_float2(keep, keep));
             }
         }
         __syncwarp();                                              // a row's 16 threads are of one warp
-        const int last = kb == j ? min(n, 4 * ty + 4) : kTok;
-        for (int s = 0; s < last; ++s) {
-            const float4 v0 = *reinterpret_cast<const float4*>(sv + s * kLd + 4 * tx);
-            const float4 v1 = *reinterpret_cast<const float4*>(sv + s * kLd + 64 + 4 * tx);
+        // keys that every row of the tile sees, four at a time; then those that some rows do not,
+        // where a masked key's value must not be touched (0 x inf is not 0)
+        const int whole = min(kKeys, max(0, diag + 1)) & ~3, last = min(ns, diag + n);
+        int s = 0;
+#pragma unroll 2
+        for (; s < whole; s += 4) {
+            float4 x[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (kb < j || s <= 4 * ty + i) {
-                    const float x = sp[(4 * ty + i) * kLdP + s];
-                    fma4(acc[i][0], x, v0);
-                    fma4(acc[i][1], x, v1);
+            for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const float4*>(sp + (4 * ty + i) * kLdP + s);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+                for (int c = 0; c < kCols; ++c) {
+                    const float4 v = *reinterpret_cast<const float4*>(sv + (s + e) * kLd + 64 * c + 4 * tx);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float w = e == 0 ? x[i].x : e == 1 ? x[i].y : e == 2 ? x[i].z : x[i].w;
+                        acc[i][c][0] = ptx::ffma2(make_float2(w, w), lo2(v), acc[i][c][0]);
+                        acc[i][c][1] = ptx::ffma2(make_float2(w, w), hi2(v), acc[i][c][1]);
+                    }
+                }
+        }
+        for (; s < last; ++s) {
+#pragma unroll
+            for (int c = 0; c < kCols; ++c) {
+                const float4 v = *reinterpret_cast<const float4*>(sv + s * kLd + 64 * c + 4 * tx);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (s <= 4 * ty + i + diag) {
+                        const float w = sp[(4 * ty + i) * kLdP + s];
+                        acc[i][c][0] = ptx::ffma2(make_float2(w, w), lo2(v), acc[i][c][0]);
+                        acc[i][c][1] = ptx::ffma2(make_float2(w, w), hi2(v), acc[i][c][1]);
+                    }
                 }
             }
         }
@@ -135,28 +172,34 @@ attn_prefill_kernel(const AttnArgs a, const Divisor block, int* err)
         if (4 * ty + i < n) {
             T* o = static_cast<T*>(a.out) + ((t0 + 4 * ty + i) * a.hq + h) * a.dim;
 #pragma unroll
-            for (int jj = 0; jj < 2; ++jj) {
-                const int c = 64 * jj + 4 * tx;
-                if (c < a.dim) {
-                    Elem<T>::store(o + c + 0, inv * acc[i][jj].x);
-                    Elem<T>::store(o + c + 1, inv * acc[i][jj].y);
-                    Elem<T>::store(o + c + 2, inv * acc[i][jj].z);
-                    Elem<T>::store(o + c + 3, inv * acc[i][jj].w);
+            for (int c = 0; c < kCols; ++c) {
+                const int col = 64 * c + 4 * tx;
+                if (col < a.dim) {
+                    Elem<T>::store(o + col + 0, inv * acc[i][c][0].x);
+                    Elem<T>::store(o + col + 1, inv * acc[i][c][0].y);
+                    Elem<T>::store(o + col + 2, inv * acc[i][c][1].x);
+                    Elem<T>::store(o + col + 3, inv * acc[i][c][1].y);
                 }
             }
         }
     }
 }
 
+template <typename T, int D>
+cudaError_t prefill_d(const AttnArgs& a, cudaStream_t s)
+{
+    constexpr int kBytes = ((kRows + 2 * kKeys) * (D + 4) + kRows * kLdP) * 4;
+    cudaError_t e = cudaFuncSetAttribute(attn_prefill_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+    if (e != cudaSuccess) return e;
+    const dim3 grid((unsigned)packed_blocks(a.total, a.nseq, kRows), (unsigned)a.hq);
+    attn_prefill_kernel<T, D><<<grid, kThreads, kBytes, s>>>(a, Divisor(kRows), device_error_word());
+    return cudaGetLastError();
+}
+
 template <typename T>
 cudaError_t prefill_t(const AttnArgs& a, cudaStream_t s)
 {
-    constexpr int kBytes = (3 * kTok * kLd + kTok * kLdP) * 4;
-    cudaError_t e = cudaFuncSetAttribute(attn_prefill_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
-    if (e != cudaSuccess) return e;
-    const dim3 grid((unsigned)packed_blocks(a.total, a.nseq, kTok), (unsigned)a.hq);
-    attn_prefill_kernel<T><<<grid, kThreads, kBytes, s>>>(a, Divisor(kTok), device_error_word());
-    return cudaGetLastError();
+    return a.dim <= 64 ? prefill_d<T, 64>(a, s) : prefill_d<T, 128>(a, s);
 }
 
 }  // namespace

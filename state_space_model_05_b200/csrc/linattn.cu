@@ -5,6 +5,8 @@
 //
 // with S a dk x dv matrix per value head; value head h reads query/key head h / (hv / hq).
 #include "mixers.cuh"
+#include "prefill_tc.h"
+#include "ptx.cuh"
 
 namespace ssd {
 
@@ -94,177 +96,248 @@ cudaError_t decode_t(float* state, const void* q, const void* k, const void* v, 
 // Blocks of 64 tokens in three launches: every block's own state U = sum_s g^(len-1-s) k_s v_s^T
 // (all blocks in parallel), a scan that turns the U into start states and writes the final
 // states, and every block's output  o_t = g^(t+1) S^T q_t + sum_{s<=t} g^(t-s) (q_t.k_s) v_s.
+// Each launch is a programmatic dependent of the one before.  Products run on packed fp32 pairs.
+// The kernels exist for dimensions padded to 64 and to 128.
 constexpr int kTok = 64;                                   // tokens per block
 constexpr int kThreads = 256;
-constexpr int kLd = kMixMaxDim + 4;                        // padded rows: 16-byte reads of 8 rows hit 8 bank quads
 constexpr int kLdP = kTok + 4;
 
-// `rows` rows of `cols` elements (a multiple of 4) into padded shared rows as fp32, zeros
-// past them up to 64 x `width`.
-template <typename T>
-__device__ __forceinline__ void load_rows(float* dst, const T* src, long long stride, int rows, int cols, int width)
+// `rows` rows of `cols` elements (a multiple of 4) into padded shared rows as fp32, zeros past
+// them.  (Rows of D + 4 floats: 16-byte reads of 8 rows hit 8 different bank quads.)
+template <typename T, int D>
+__device__ __forceinline__ void load_rows(float* dst, const T* src, long long stride, int rows, int cols)
 {
-    const int quads = width / 4;
-    for (int i = threadIdx.x; i < kTok * quads; i += kThreads) {
-        const int r = i / quads, c = 4 * (i - r * quads);
+#pragma unroll 4
+    for (int i = threadIdx.x; i < kTok * (D / 4); i += kThreads) {
+        const int r = i / (D / 4), c = 4 * (i % (D / 4));
         const float4 x = (r < rows && c < cols) ? load4<T>(src + (size_t)r * stride + c) : make_float4(0.f, 0.f, 0.f, 0.f);
-        *reinterpret_cast<float4*>(dst + r * kLd + c) = x;
+        *reinterpret_cast<float4*>(dst + r * (D + 4) + c) = x;
     }
 }
 
-__device__ __forceinline__ void fma4(float4& a, float s, const float4& b)
-{
-    a.x = fmaf(s, b.x, a.x); a.y = fmaf(s, b.y, a.y); a.z = fmaf(s, b.z, a.z); a.w = fmaf(s, b.w, a.w);
-}
+__device__ __forceinline__ float2 lo2(const float4& x) { return make_float2(x.x, x.y); }
+__device__ __forceinline__ float2 hi2(const float4& x) { return make_float2(x.z, x.w); }
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
-template <typename T>
+template <typename T, int DK, int DV>
 __global__ void __launch_bounds__(kThreads)
 linattn_block_state_kernel(const LinattnArgs a, const Divisor block, float* __restrict__ states, int* err)
 {
+    constexpr int kLdK = DK + 4, kLdV = DV + 4, kR = DK / 16, kC = DV / 64;   // thread: kR rows, 4 kC columns
     extern __shared__ float sm[];
-    float *sk = sm, *sv = sm + kTok * kLd;
+    __shared__ float sw[kTok];
+    float *sk = sm, *sv = sm + kTok * kLdK;
     const int h = blockIdx.y, tid = threadIdx.x;
+    ptx::griddep_launch_dependents();
     if (blockIdx.x == 0 && h == 0) check_offsets(a.cu, a.nseq, a.total, err);
     int seq, j, first, len;
     if (!packed_block(a.cu, a.nseq, a.total, block, blockIdx.x, err, &seq, &j, &first, &len)) return;
     const int n = min(kTok, len - j * kTok);
     if (n <= 0) return;
     const size_t t0 = (size_t)first + (size_t)j * kTok;
-    const float ld = a.log_decay[h];
-    load_rows<T>(sk, static_cast<const T*>(a.k) + t0 * a.k_stride + (size_t)(h / (a.hv / a.hq)) * a.dk, a.k_stride, n,
-                 a.dk, kMixMaxDim);
-    load_rows<T>(sv, static_cast<const T*>(a.v) + t0 * a.v_stride + (size_t)h * a.dv, a.v_stride, n, a.dv, kMixMaxDim);
+    if (tid < n) sw[tid] = decay_pow(a.log_decay[h], n - 1 - tid);
+    load_rows<T, DK>(sk, static_cast<const T*>(a.k) + t0 * a.k_stride + (size_t)(h / (a.hv / a.hq)) * a.dk, a.k_stride, n, a.dk);
+    load_rows<T, DV>(sv, static_cast<const T*>(a.v) + t0 * a.v_stride + (size_t)h * a.dv, a.v_stride, n, a.dv);
     __syncthreads();
-    // thread: rows 8 ty .. + 7, columns 4 tx .. + 3 and 64 + 4 tx .. + 3
+    // rows kR ty .. + kR - 1, columns 4 tx .. + 3 (and 64 + 4 tx .. + 3)
     const int tx = tid & 15, ty = tid >> 4;
-    float4 acc[8][2];
+    float2 acc[kR][kC][2];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i][0] = acc[i][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < kR; ++i)
+#pragma unroll
+        for (int c = 0; c < kC; ++c) acc[i][c][0] = acc[i][c][1] = make_float2(0.f, 0.f);
+#pragma unroll 4
     for (int s = 0; s < n; ++s) {
-        const float w = decay_pow(ld, n - 1 - s);
-        const float4 k0 = *reinterpret_cast<const float4*>(sk + s * kLd + 8 * ty);
-        const float4 k1 = *reinterpret_cast<const float4*>(sk + s * kLd + 8 * ty + 4);
-        const float4 v0 = *reinterpret_cast<const float4*>(sv + s * kLd + 4 * tx);
-        const float4 v1 = *reinterpret_cast<const float4*>(sv + s * kLd + 64 + 4 * tx);
-        const float kk[8] = {k0.x, k0.y, k0.z, k0.w, k1.x, k1.y, k1.z, k1.w};
+        const float w = sw[s];
+        float kk[kR];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            fma4(acc[i][0], w * kk[i], v0);
-            fma4(acc[i][1], w * kk[i], v1);
+        for (int i = 0; i < kR; i += 4) {
+            const float4 x = *reinterpret_cast<const float4*>(sk + s * kLdK + kR * ty + i);
+            kk[i] = w * x.x; kk[i + 1] = w * x.y; kk[i + 2] = w * x.z; kk[i + 3] = w * x.w;
+        }
+#pragma unroll
+        for (int c = 0; c < kC; ++c) {
+            const float4 v = *reinterpret_cast<const float4*>(sv + s * kLdV + 64 * c + 4 * tx);
+#pragma unroll
+            for (int i = 0; i < kR; ++i) {
+                acc[i][c][0] = ptx::ffma2(both(kk[i]), lo2(v), acc[i][c][0]);
+                acc[i][c][1] = ptx::ffma2(both(kk[i]), hi2(v), acc[i][c][1]);
+            }
         }
     }
     float* U = states + ((size_t)blockIdx.x * a.hv + h) * a.dk * a.dv;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int r = 8 * ty + i;
-        if (r < a.dk) {
-            if (4 * tx < a.dv) *reinterpret_cast<float4*>(U + (size_t)r * a.dv + 4 * tx) = acc[i][0];
-            if (64 + 4 * tx < a.dv) *reinterpret_cast<float4*>(U + (size_t)r * a.dv + 64 + 4 * tx) = acc[i][1];
-        }
+    for (int i = 0; i < kR; ++i) {
+        const int r = kR * ty + i;
+#pragma unroll
+        for (int c = 0; c < kC; ++c)
+            if (r < a.dk && 64 * c + 4 * tx < a.dv)
+                *reinterpret_cast<float4*>(U + (size_t)r * a.dv + 64 * c + 4 * tx) =
+                    make_float4(acc[i][c][0].x, acc[i][c][0].y, acc[i][c][1].x, acc[i][c][1].y);
     }
 }
 
-// Start state of every block (over its U) and the final state, four elements a thread.
-__global__ void __launch_bounds__(kThreads)
-linattn_scan_kernel(const LinattnArgs a, float* __restrict__ states, int* err)
+// Start state of every block (over its U) and the final state, four elements a thread.  The
+// next blocks' U are loaded ahead of the chain.
+constexpr int kScanThreads = 64, kAhead = 4;
+
+__global__ void __launch_bounds__(kScanThreads)
+linattn_scan_kernel(const LinattnArgs a, float* states)
 {
     const int seq = blockIdx.x / a.hv, h = blockIdx.x - seq * a.hv;
-    const int e = (blockIdx.y * kThreads + threadIdx.x) * 4, elems = a.dk * a.dv;
-    if (e >= elems) return;
+    const int e = (blockIdx.y * kScanThreads + threadIdx.x) * 4, elems = a.dk * a.dv;
+    ptx::griddep_launch_dependents();
     const int first = a.cu[seq], len = a.cu[seq + 1] - first;
-    if (first < 0 || len < 0 || first + len > a.total) return;      // reported by the blocks
     const float ld = a.log_decay[h];
     const size_t base = (size_t)blockIdx.x * elems + e;
-    float4 H = a.init_states ? *reinterpret_cast<const float4*>(a.init_states + base) : make_float4(0.f, 0.f, 0.f, 0.f);
+    float4 H = a.init_states && e < elems ? *reinterpret_cast<const float4*>(a.init_states + base) : make_float4(0.f, 0.f, 0.f, 0.f);
+    ptx::griddep_wait();
+    if (e >= elems || first < 0 || len < 0 || first + len > a.total) return;      // (offsets reported by the blocks)
     float* U = states + ((size_t)(first / kTok + seq) * a.hv + h) * elems + e;
     const size_t step = (size_t)a.hv * elems;
-    for (int t = 0; t < len; t += kTok, U += step) {
-        const float4 u = *reinterpret_cast<const float4*>(U);
-        *reinterpret_cast<float4*>(U) = H;
-        const float g = decay_pow(ld, min(kTok, len - t));
-        H.x = fmaf(g, H.x, u.x); H.y = fmaf(g, H.y, u.y); H.z = fmaf(g, H.z, u.z); H.w = fmaf(g, H.w, u.w);
+    const int blocks = (len + kTok - 1) / kTok;
+    const float whole = decay_pow(ld, kTok);
+    float4 u[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+        if (i < blocks) u[i] = *reinterpret_cast<const float4*>(U + i * step);
+    for (int t = 0; t < blocks; t += kAhead) {
+        float4 next[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (t + kAhead + i < blocks) next[i] = *reinterpret_cast<const float4*>(U + (size_t)(t + kAhead + i) * step);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            if (t + i >= blocks) break;
+            *reinterpret_cast<float4*>(U + (size_t)(t + i) * step) = H;
+            const float g = t + i + 1 < blocks ? whole : decay_pow(ld, len - (t + i) * kTok);
+            H.x = fmaf(g, H.x, u[i].x); H.y = fmaf(g, H.y, u[i].y); H.z = fmaf(g, H.z, u[i].z); H.w = fmaf(g, H.w, u[i].w);
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) u[i] = next[i];
     }
     *reinterpret_cast<float4*>(a.final_states + base) = H;
 }
 
-template <typename T>
+template <typename T, int DK, int DV>
 __global__ void __launch_bounds__(kThreads)
 linattn_block_output_kernel(const LinattnArgs a, const Divisor block, const float* __restrict__ states, int* err)
 {
+    constexpr int kLdK = DK + 4, kLdV = DV + 4, kC = DV / 64;
     extern __shared__ float sm[];
-    float *sq = sm, *sk = sq + kTok * kLd, *sv = sk + kTok * kLd, *sp = sv + kTok * kLd;
+    __shared__ float sg[kTok + 1];                         // g^0 .. g^64
+    float *sq = sm, *sk = sq + kTok * kLdK, *sv = sk + kTok * kLdK, *sp = sv + kTok * kLdV;
+    float* ss = sk;                                        // 64 rows of the start state, in the keys' place
     const int h = blockIdx.y, tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     int seq, j, first, len;
-    if (!packed_block(a.cu, a.nseq, a.total, block, blockIdx.x, err, &seq, &j, &first, &len)) return;
-    const int n = min(kTok, len - j * kTok);
-    if (n <= 0) return;
+    const bool valid = packed_block(a.cu, a.nseq, a.total, block, blockIdx.x, err, &seq, &j, &first, &len);
+    const int n = valid ? min(kTok, len - j * kTok) : 0;
+    if (n <= 0) {
+        ptx::griddep_wait();                               // (this grid ends after the one before)
+        return;
+    }
     const size_t t0 = (size_t)first + (size_t)j * kTok;
-    const float ld = a.log_decay[h];
     const size_t hk = (size_t)(h / (a.hv / a.hq)) * a.dk;
-    load_rows<T>(sq, static_cast<const T*>(a.q) + t0 * a.q_stride + hk, a.q_stride, n, a.dk, kMixMaxDim);
-    load_rows<T>(sk, static_cast<const T*>(a.k) + t0 * a.k_stride + hk, a.k_stride, n, a.dk, kMixMaxDim);
-    load_rows<T>(sv, static_cast<const T*>(a.v) + t0 * a.v_stride + (size_t)h * a.dv, a.v_stride, n, a.dv, kMixMaxDim);
+    if (tid <= kTok) sg[tid] = decay_pow(a.log_decay[h], tid);
+    load_rows<T, DK>(sq, static_cast<const T*>(a.q) + t0 * a.q_stride + hk, a.q_stride, n, a.dk);
+    load_rows<T, DK>(sk, static_cast<const T*>(a.k) + t0 * a.k_stride + hk, a.k_stride, n, a.dk);
+    load_rows<T, DV>(sv, static_cast<const T*>(a.v) + t0 * a.v_stride + (size_t)h * a.dv, a.v_stride, n, a.dv);
     __syncthreads();
     // scores: thread rows t = 4 ty + i, columns s = tx + 16 jj
-    float p[4][4] = {};
+    float2 p[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int jj = 0; jj < 4; ++jj) p[i][jj] = make_float2(0.f, 0.f);
+#pragma unroll 2
     for (int d = 0; d < a.dk; d += 4) {
         float4 x[4], y[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const float4*>(sq + (4 * ty + i) * kLd + d);
+        for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const float4*>(sq + (4 * ty + i) * kLdK + d);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = *reinterpret_cast<const float4*>(sk + (tx + 16 * i) * kLd + d);
+        for (int i = 0; i < 4; ++i) y[i] = *reinterpret_cast<const float4*>(sk + (tx + 16 * i) * kLdK + d);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int jj = 0; jj < 4; ++jj)
-                p[i][jj] = fmaf(x[i].x, y[jj].x, fmaf(x[i].y, y[jj].y, fmaf(x[i].z, y[jj].z, fmaf(x[i].w, y[jj].w, p[i][jj]))));
+                p[i][jj] = ptx::ffma2(hi2(x[i]), hi2(y[jj]), ptx::ffma2(lo2(x[i]), lo2(y[jj]), p[i][jj]));
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int jj = 0; jj < 4; ++jj) {
             const int t = 4 * ty + i, s = tx + 16 * jj;
-            sp[t * kLdP + s] = s <= t ? p[i][jj] * decay_pow(ld, t - s) : 0.f;
+            sp[t * kLdP + s] = s <= t ? (p[i][jj].x + p[i][jj].y) * sg[t - s] : 0.f;
         }
-    // the carried part: acc = S^T q, 64 rows of S at a time in the keys' place
+    // the carried part: acc = S^T q, 64 rows of S at a time
     const float* S = states + ((size_t)blockIdx.x * a.hv + h) * a.dk * a.dv;
-    float4 acc[4][2];
+    float2 acc[4][kC][2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[i][0] = acc[i][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int c = 0; c < kC; ++c) acc[i][c][0] = acc[i][c][1] = make_float2(0.f, 0.f);
+    ptx::griddep_wait();                                   // the start states come from the kernel before
     for (int d0 = 0; d0 < a.dk; d0 += kTok) {
         __syncthreads();
-        load_rows<float>(sk, S + (size_t)d0 * a.dv, a.dv, min(kTok, a.dk - d0), a.dv, kMixMaxDim);
+        load_rows<float, DV>(ss, S + (size_t)d0 * a.dv, a.dv, min(kTok, a.dk - d0), a.dv);
         __syncthreads();
-        for (int d = 0; d < min(kTok, a.dk - d0); ++d) {
-            const float4 v0 = *reinterpret_cast<const float4*>(sk + d * kLd + 4 * tx);
-            const float4 v1 = *reinterpret_cast<const float4*>(sk + d * kLd + 64 + 4 * tx);
+#pragma unroll 2
+        for (int d = 0; d < min(kTok, a.dk - d0); d += 4) {        // dk is a multiple of 8
+            float4 x[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const float4*>(sq + (4 * ty + i) * kLdK + d0 + d);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+                for (int c = 0; c < kC; ++c) {
+                    const float4 v = *reinterpret_cast<const float4*>(ss + (d + e) * kLdV + 64 * c + 4 * tx);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float w = e == 0 ? x[i].x : e == 1 ? x[i].y : e == 2 ? x[i].z : x[i].w;
+                        acc[i][c][0] = ptx::ffma2(both(w), lo2(v), acc[i][c][0]);
+                        acc[i][c][1] = ptx::ffma2(both(w), hi2(v), acc[i][c][1]);
+                    }
+                }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int c = 0; c < kC; ++c) {
+            acc[i][c][0] = ptx::fmul2(acc[i][c][0], both(sg[4 * ty + i + 1]));
+            acc[i][c][1] = ptx::fmul2(acc[i][c][1], both(sg[4 * ty + i + 1]));
+        }
+    // the block's own part: rows s <= t of v (those before the thread's rows for all four alike)
+    int s = 0;
+#pragma unroll 2
+    for (; s < min(n, 4 * ty) / 4 * 4; s += 4) {
+        float4 x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const float4*>(sp + (4 * ty + i) * kLdP + s);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int c = 0; c < kC; ++c) {
+                const float4 v = *reinterpret_cast<const float4*>(sv + (s + e) * kLdV + 64 * c + 4 * tx);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float w = e == 0 ? x[i].x : e == 1 ? x[i].y : e == 2 ? x[i].z : x[i].w;
+                    acc[i][c][0] = ptx::ffma2(both(w), lo2(v), acc[i][c][0]);
+                    acc[i][c][1] = ptx::ffma2(both(w), hi2(v), acc[i][c][1]);
+                }
+            }
+    }
+    for (; s < min(n, 4 * ty + 4); ++s) {
+#pragma unroll
+        for (int c = 0; c < kC; ++c) {
+            const float4 v = *reinterpret_cast<const float4*>(sv + s * kLdV + 64 * c + 4 * tx);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float x = sq[(4 * ty + i) * kLd + d0 + d];
-                fma4(acc[i][0], x, v0);
-                fma4(acc[i][1], x, v1);
-            }
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float g = decay_pow(ld, 4 * ty + i + 1);
-#pragma unroll
-        for (int jj = 0; jj < 2; ++jj) {
-            float4& x = acc[i][jj];
-            x.x *= g; x.y *= g; x.z *= g; x.w *= g;
-        }
-    }
-    // the block's own part: rows s <= t of v
-    for (int s = 0; s < min(n, 4 * ty + 4); ++s) {
-        const float4 v0 = *reinterpret_cast<const float4*>(sv + s * kLd + 4 * tx);
-        const float4 v1 = *reinterpret_cast<const float4*>(sv + s * kLd + 64 + 4 * tx);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (s <= 4 * ty + i) {
-                const float x = sp[(4 * ty + i) * kLdP + s];
-                fma4(acc[i][0], x, v0);
-                fma4(acc[i][1], x, v1);
+                if (s <= 4 * ty + i) {
+                    const float w = sp[(4 * ty + i) * kLdP + s];
+                    acc[i][c][0] = ptx::ffma2(both(w), lo2(v), acc[i][c][0]);
+                    acc[i][c][1] = ptx::ffma2(both(w), hi2(v), acc[i][c][1]);
+                }
             }
         }
     }
@@ -273,35 +346,46 @@ linattn_block_output_kernel(const LinattnArgs a, const Divisor block, const floa
         if (4 * ty + i < n) {
             T* o = static_cast<T*>(a.out) + ((t0 + 4 * ty + i) * a.hv + h) * a.dv;
 #pragma unroll
-            for (int jj = 0; jj < 2; ++jj) {
-                const int c = 64 * jj + 4 * tx;
-                if (c < a.dv) {
-                    Elem<T>::store(o + c + 0, a.scale * acc[i][jj].x);
-                    Elem<T>::store(o + c + 1, a.scale * acc[i][jj].y);
-                    Elem<T>::store(o + c + 2, a.scale * acc[i][jj].z);
-                    Elem<T>::store(o + c + 3, a.scale * acc[i][jj].w);
+            for (int c = 0; c < kC; ++c) {
+                const int col = 64 * c + 4 * tx;
+                if (col < a.dv) {
+                    Elem<T>::store(o + col + 0, a.scale * acc[i][c][0].x);
+                    Elem<T>::store(o + col + 1, a.scale * acc[i][c][0].y);
+                    Elem<T>::store(o + col + 2, a.scale * acc[i][c][1].x);
+                    Elem<T>::store(o + col + 3, a.scale * acc[i][c][1].y);
                 }
             }
         }
     }
 }
 
-template <typename T>
-cudaError_t prefill_t(const LinattnArgs& a, float* states, cudaStream_t s)
+template <typename T, int DK, int DV>
+cudaError_t prefill_d(const LinattnArgs& a, float* states, cudaStream_t s)
 {
-    constexpr int kStateBytes = 2 * kTok * kLd * 4, kOutBytes = (3 * kTok * kLd + kTok * kLdP) * 4;
-    cudaError_t e = cudaFuncSetAttribute(linattn_block_state_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         kStateBytes);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(linattn_block_output_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kOutBytes);
+    constexpr int kStateBytes = kTok * (DK + DV + 8) * 4;
+    constexpr int kOutBytes = kTok * (2 * (DK + 4) + DV + 4 + kLdP) * 4;
+    static_assert(DK >= DV, "the rows of the start state fit into the place of the keys");
+    auto state_kernel = linattn_block_state_kernel<T, DK, DV>;
+    auto output_kernel = linattn_block_output_kernel<T, DK, DV>;
+    cudaError_t e = cudaFuncSetAttribute(state_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kStateBytes);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(output_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kOutBytes);
     if (e != cudaSuccess) return e;
     int* err = device_error_word();
     const dim3 grid((unsigned)packed_blocks(a.total, a.nseq, kTok), (unsigned)a.hv);
-    linattn_block_state_kernel<T><<<grid, kThreads, kStateBytes, s>>>(a, Divisor(kTok), states, err);
-    const dim3 scan((unsigned)(a.nseq * a.hv), (unsigned)((a.dk * a.dv + 4 * kThreads - 1) / (4 * kThreads)));
-    linattn_scan_kernel<<<scan, kThreads, 0, s>>>(a, states, err);
-    if (a.total > 0) linattn_block_output_kernel<T><<<grid, kThreads, kOutBytes, s>>>(a, Divisor(kTok), states, err);
-    return cudaGetLastError();
+    state_kernel<<<grid, kThreads, kStateBytes, s>>>(a, Divisor(kTok), states, err);
+    e = cudaGetLastError();
+    const dim3 scan((unsigned)(a.nseq * a.hv), (unsigned)((a.dk * a.dv + 4 * kScanThreads - 1) / (4 * kScanThreads)));
+    if (e == cudaSuccess) e = launch_dependent(linattn_scan_kernel, scan, dim3(kScanThreads), 0, s, a, states);
+    if (e == cudaSuccess && a.total > 0)
+        e = launch_dependent(output_kernel, grid, dim3(kThreads), kOutBytes, s, a, Divisor(kTok), static_cast<const float*>(states), err);
+    return e;
+}
+
+template <typename T>
+cudaError_t prefill_t(const LinattnArgs& a, float* states, cudaStream_t s)
+{
+    if (a.dk <= 64 && a.dv <= 64) return prefill_d<T, 64, 64>(a, states, s);
+    return a.dv <= 64 ? prefill_d<T, 128, 64>(a, states, s) : prefill_d<T, 128, 128>(a, states, s);
 }
 
 }  // namespace
