@@ -140,20 +140,20 @@ def _rank(t: torch.Tensor, name: str, layout: str):
 def _check_args(ref: torch.Tensor, specs):
     """Validate the tensors of one call before anything reaches the library, which sees only
     pointers and so cannot tell a short buffer from a right one.  ``specs`` holds
-    (tensor or None, name, expected shape, dtype or None); every tensor given must have that
-    shape, live on ``ref``'s device, be a contiguous CUDA tensor and (if stated) have that
+    (tensor or None, name, expected shape or None for any, dtype or None); every tensor given must
+    have that shape, live on ``ref``'s device, be a contiguous CUDA tensor and (if stated) have that
     dtype.  ``ref`` must be on the current device, whose stream the library launches on."""
     if ref.is_cuda:                                # the usual case: nothing to report
         device = ref.get_device()
         for t, _, shape, dtype in specs:
-            if t is not None and (t.shape != shape or not t.is_cuda or t.get_device() != device
-                                  or (dtype is not None and t.dtype != dtype) or not t.is_contiguous()):
+            if t is not None and not ((shape is None or t.shape == shape) and (dtype is None or t.dtype is dtype)
+                                      and t.get_device() == device and t.is_contiguous() and t.is_cuda):
                 break
         else:
             if device == torch._C._cuda_getDevice():
                 return
     for t, name, shape, _ in specs:
-        if t is not None and tuple(t.shape) != tuple(shape):
+        if t is not None and shape is not None and tuple(t.shape) != tuple(shape):
             raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     for t, name, _, dtype in specs:
         if t is None:
@@ -368,13 +368,15 @@ def _packed(t: torch.Tensor) -> int:
     """Elements from one token of ``t`` [tokens][heads][dim] to the next, for a tensor whose
     tokens may lie apart (a slice of a fused projection); each token's own elements may not."""
     (tokens, heads, dim), (apart, head, one) = t.shape, t.stride()
+    if one == 1 and head == dim and tokens > 1:
+        return apart
     if t.numel() and ((dim > 1 and one != 1) or (heads > 1 and head != dim)):
         raise ValueError("the heads of a token must be contiguous")
     return apart if tokens > 1 else heads * dim
 
 
 def _nseq(cu_seqlens: torch.Tensor) -> int:
-    n = cu_seqlens.numel()
+    n = cu_seqlens.shape[0]
     if n < 2:
         raise ValueError("cu_seqlens holds nseq + 1 offsets, at least two")
     return n - 1
@@ -389,7 +391,7 @@ def _check_mixer(ref: torch.Tensor, strided, specs):
     _check_args(ref, specs)
     dtype, device = ref.dtype, ref.get_device()
     for t, name, _ in strided:
-        if t.dtype == dtype and t.get_device() == device and t.is_cuda:
+        if t.dtype is dtype and t.get_device() == device and t.is_cuda:
             continue
         if not t.is_cuda:
             raise ValueError(f"{name} must be a CUDA tensor")
@@ -414,23 +416,21 @@ def ssd_linattn_prefill(q, k, v, log_decay, cu_seqlens, scale=1.0, init_states=N
     _rank(q, "q", "[tokens][heads_qk][dk]")
     _rank(v, "v", "[tokens][heads_v][dv]")
     _rank(cu_seqlens, "cu_seqlens", "[nseq + 1]")
-    total, hq, dk = q.shape
-    hv, dv = v.shape[1], v.shape[2]
-    nseq = _nseq(cu_seqlens)
-    f32, key_shape, out_shape, state_shape = torch.float32, (total, hq, dk), (total, hv, dv), (nseq, hv, dk, dv)
-    _check_mixer(q, ((q, "q", key_shape), (k, "k", key_shape), (v, "v", out_shape)),
+    key_shape, out_shape, nseq, dtype = q.shape, v.shape, _nseq(cu_seqlens), q.dtype
+    (total, hq, dk), (_, hv, dv) = key_shape, out_shape
+    f32, state_shape = torch.float32, (nseq, hv, dk, dv)
+    _check_mixer(q, ((q, "q", key_shape), (k, "k", key_shape), (v, "v", (total, hv, dv))),
                  ((log_decay, "log_decay", (hv,), f32), (cu_seqlens, "cu_seqlens", (nseq + 1,), torch.int32),
-                  (init_states, "init_states", state_shape, f32), (out, "out", out_shape, q.dtype),
-                  (final_states, "final_states", state_shape, f32),
-                  (workspace, "workspace", workspace.shape if workspace is not None else (), None)))
-    code = _dtype_code(q)
+                  (init_states, "init_states", state_shape, f32), (out, "out", out_shape, dtype),
+                  (final_states, "final_states", state_shape, f32), (workspace, "workspace", None, None)))
+    code, device = _dtype_code(q), q.device
     if out is None:
-        out = torch.empty(out_shape, dtype=q.dtype, device=q.device)
+        out = torch.empty(out_shape, dtype=dtype, device=device)
     if final_states is None:
-        final_states = torch.empty(state_shape, dtype=f32, device=q.device)
+        final_states = torch.empty(state_shape, dtype=f32, device=device)
     if workspace is None:
-        need = _workspace_bytes("ssd_linattn_prefill_workspace_bytes", nseq, total, hq, hv, dk, dv, code)
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = torch.empty(_workspace_bytes("ssd_linattn_prefill_workspace_bytes", nseq, total, hq, hv, dk, dv, code),
+                                dtype=torch.uint8, device=device)
     st = lib().ssd_linattn_prefill(_ptr(q), _ptr(k), _ptr(v), _packed(q), _packed(k), _packed(v), _ptr(log_decay),
                                    _ptr(init_states), _ptr(cu_seqlens), nseq, total, hq, hv, dk, dv, scale, code,
                                    _ptr(out), _ptr(final_states), _ptr(workspace), _nbytes(workspace), _stream(stream))
@@ -466,9 +466,9 @@ def ssd_attn_prefill(q, k, v, cu_seqlens, scale=None, out=None, stream=None):
     _rank(q, "q", "[tokens][heads_q][headdim]")
     _rank(k, "k", "[tokens][heads_kv][headdim]")
     _rank(cu_seqlens, "cu_seqlens", "[nseq + 1]")
-    total, hq, dim = q.shape
-    hkv, nseq = k.shape[1], _nseq(cu_seqlens)
-    out_shape, key_shape = (total, hq, dim), (total, hkv, dim)
+    out_shape, hkv, nseq = q.shape, k.shape[1], _nseq(cu_seqlens)
+    total, hq, dim = out_shape
+    key_shape = (total, hkv, dim)
     _check_mixer(q, ((q, "q", out_shape), (k, "k", key_shape), (v, "v", key_shape)),
                  ((cu_seqlens, "cu_seqlens", (nseq + 1,), torch.int32), (out, "out", out_shape, q.dtype)))
     code = _dtype_code(q)
@@ -495,13 +495,13 @@ def ssd_attn_decode_step(k_cache, v_cache, cache_lens, q, k, v, scale=None, out=
     _check_args(q, ((k_cache, "k_cache", cache, dtype), (v_cache, "v_cache", cache, dtype),
                     (cache_lens, "cache_lens", (batch,), torch.int32), (q, "q", rows, dtype),
                     (k, "k", new, dtype), (v, "v", new, dtype), (out, "out", rows, dtype),
-                    (workspace, "workspace", workspace.shape if workspace is not None else (), None)))
+                    (workspace, "workspace", None, None)))
     code = _dtype_code(q)
     if out is None:
         out = torch.empty_like(q)
     if workspace is None:
-        need = _workspace_bytes("ssd_attn_decode_workspace_bytes", batch, capacity, hq, hkv, dim, code)
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = torch.empty(_workspace_bytes("ssd_attn_decode_workspace_bytes", batch, capacity, hq, hkv, dim, code),
+                                dtype=torch.uint8, device=q.device)
     st = lib().ssd_attn_decode_step(_ptr(k_cache), _ptr(v_cache), _ptr(cache_lens), _ptr(q), _ptr(k), _ptr(v), batch,
                                     capacity, hq, hkv, dim, dim ** -0.5 if scale is None else scale, code, _ptr(out),
                                     _ptr(workspace), _nbytes(workspace), _stream(stream))
