@@ -43,6 +43,32 @@ struct Units {
 };
 
 // ---- ranges of tiles -----------------------------------------------------------------
+// a / b, in 32 bits where both fit (a 64-bit division is a hundred instructions, cold ones here).
+__device__ __forceinline__ long long quotient(long long a, long long b)
+{
+    return (a | b) >> 32 ? a / b : (long long)((unsigned)a / (unsigned)b);
+}
+
+// W tiles over at most `ctas` CTAs: the first W mod G take one more than the others, and no
+// range is empty.
+struct Ranges {
+    long long W, each;
+    int G, more;
+    __device__ __forceinline__ Ranges(long long tiles, int ctas) : W(tiles), each(0), G((int)min((long long)ctas, tiles)), more(0)
+    {
+        if (G > 0) {
+            each = quotient(W, G);
+            more = (int)(W - each * G);
+        }
+    }
+    __device__ __forceinline__ long long first(int c) const { return each * c + min(c, more); }
+    __device__ __forceinline__ int owner(long long t) const         // the CTA whose range holds tile t
+    {
+        const long long longer = (each + 1) * more;
+        return (int)(t < longer ? quotient(t, each + 1) : more + quotient(t - longer, each));
+    }
+};
+
 // Tiles of all rows and of those before one row, found by the threads of a CTA together.
 struct Located { int b; long long before, total; };
 
@@ -104,7 +130,7 @@ struct Cursor {
         len = lens[b];
         n = row_tiles(len, capacity);
         const long long y = x - at.before * units;
-        u = (int)(y / n);
+        u = (int)quotient(y, n);
         tile = (int)(y - (long long)u * n);
     }
     __device__ __forceinline__ void next(const int* lens, int capacity, int units, bool more)
@@ -190,15 +216,14 @@ attn_decode_bf16_kernel(const __grid_constant__ CacheMaps maps, const AttnDecode
     griddep_launch_dependents();
     const Units un(a.hq, a.hkv, kRows);
     const int c = blockIdx.x;
-    auto ctas = [&](long long total) { return min((long long)gridDim.x, total * un.per_row); };   // no range is empty
     const Located at = locate<kThreads>(a.lens, a.batch, a.capacity, un.per_row, false, c == 0 ? err : nullptr,
                                         [&](long long total) {
-                                            const long long G = ctas(total);
-                                            return c < G ? total * un.per_row * c / G : -1;
+                                            const Ranges r(total * un.per_row, gridDim.x);
+                                            return c < r.G ? r.first(c) : -1;
                                         });
-    const long long W = at.total * un.per_row, G = ctas(at.total);
-    if (c >= G) return;
-    const long long x0 = W * c / G, x1 = W * (c + 1) / G;
+    const Ranges ranges(at.total * un.per_row, gridDim.x);
+    if (c >= ranges.G) return;
+    const long long x0 = ranges.first(c), x1 = ranges.first(c + 1);
     Cursor cur;
     cur.start(a.lens, a.capacity, at, x0, un.per_row);
     auto wait = [&](uint64_t* bar, int phase) { return mbar_wait_compact(bar, phase & 1, err, abort_flag); };
@@ -429,15 +454,14 @@ attn_decode_f32_kernel(const AttnDecodeArgs a, float* __restrict__ pieces, int* 
     griddep_launch_dependents();
     const int tid = threadIdx.x, c = blockIdx.x;
     const Units un(a.hq, a.hkv, kRows32);
-    auto ctas = [&](long long total) { return min((long long)gridDim.x, total * un.per_row); };   // no range is empty
     const Located at = locate<kThreads32>(a.lens, a.batch, a.capacity, un.per_row, false, c == 0 ? err : nullptr,
-                                          [&](long long total) {
-                                              const long long G = ctas(total);
-                                              return c < G ? total * un.per_row * c / G : -1;
-                                          });
-    const long long W = at.total * un.per_row, G = ctas(at.total);
-    if (c >= G) return;
-    const long long x0 = W * c / G, x1 = W * (c + 1) / G;
+                                        [&](long long total) {
+                                            const Ranges r(total * un.per_row, gridDim.x);
+                                            return c < r.G ? r.first(c) : -1;
+                                        });
+    const Ranges ranges(at.total * un.per_row, gridDim.x);
+    if (c >= ranges.G) return;
+    const long long x0 = ranges.first(c), x1 = ranges.first(c + 1);
     Cursor cur;
     cur.start(a.lens, a.capacity, at, x0, un.per_row);
     bool from_start = cur.tile == 0, fresh = true;
@@ -566,16 +590,14 @@ attn_decode_join_kernel(const AttnDecodeArgs a, const float* __restrict__ pieces
     const int hk = h / un.group, r = (h - hk * un.group) % kUnitRows, u = hk * un.blocks + (h - hk * un.group) / kUnitRows;
     const Located at = locate<kMixMaxDim>(a.lens, a.batch, a.capacity, un.per_row, true, nullptr, [&](long long) { return (long long)b; });
     const int n = row_tiles(a.lens[b], a.capacity);
-    griddep_wait();                                        // also where nothing is to join: this grid ends after the one before
-    if (n == 0) return;
-    const long long W = at.total * un.per_row, G = min((long long)max_ctas, W);
+    if (n == 0) {
+        griddep_wait();                                    // also where nothing is to join: this grid ends after the one before
+        return;
+    }
+    const Ranges ranges(at.total * un.per_row, max_ctas);
     const long long t0 = at.before * un.per_row + (long long)u * n, t1 = t0 + n;
-    auto owner = [&](long long t) {                        // the CTA whose range holds tile t
-        long long c = t * G / W;
-        while (W * (c + 1) / G <= t) ++c;
-        return (int)c;
-    };
-    const int c0 = owner(t0), c1 = owner(t1 - 1);
+    const int c0 = ranges.owner(t0), c1 = ranges.owner(t1 - 1);
+    griddep_wait();
     if (c0 == c1) return;
     // the piece that starts at its unit's start lies in its CTA's second slot
     auto piece = [&](int c) { return pieces + (size_t)(2 * c + (c == c0 ? 1 : 0)) * kPiece<kUnitRows>; };
