@@ -3,7 +3,7 @@
 //
 //     o_t = sum_{s<=t} p_s v_s / sum_{s<=t} p_s,   p_s = 2^(c q_t.k_s - m),   c = scale log2(e)
 //
-// One CTA takes 256 query rows of one key/value head, as two tiles of 128 rows.  A row is a
+// A CTA takes 256 query rows of one key/value head at a time, as two tiles of 128 rows.  A row is a
 // (token, query head of the group) pair, so the heads that share a key/value head share its
 // loads and a tile spans 128 / group tokens, which also keeps the masked part of the last key
 // tile small.  Keys are visited 128 at a time.  Per key tile i and query tile j:
@@ -36,7 +36,8 @@ constexpr int kKeys = 128;                                 // keys per tile
 constexpr int kHalf = kKeys * 128;                         // one 64-dimension half of a tile, 128-byte rows
 constexpr int kThreads = 384;                              // 8 softmax warps, TMA, 2 MMA, values
 constexpr int kWarpTma = 8, kWarpMma = 9, kWarpValues = 11;
-constexpr int kMaxMasked = 3;                              // key tiles that hold a diagonal of the CTA
+constexpr int kMaxMasked = 3;                              // key tiles that hold a diagonal of the block
+constexpr int kFixedBars = 16 + 4 * kMaxMasked;            // barriers before those of the K and V tiles
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kSlack = 8.f;                              // log2 of the largest p before the maximum moves
 
@@ -44,11 +45,13 @@ template <int D>
 struct Cfg {
     static constexpr int kHalves = D / 64;
     static constexpr int kTile = kHalves * kHalf;          // bytes of a Q, K or V tile
-    static constexpr int kSlots = D == 128 ? 5 : 8;        // K and V tiles in flight
+    static constexpr int kSlots = D == 128 ? 4 : 8;        // K and V tiles in flight
     static constexpr int kKv = 2 * kTile;
-    static constexpr int kBar = kKv + kSlots * kTile;
-    static constexpr int kNumBars = 1 + 2 * kSlots + 8 + 2 * kMaxMasked;
-    static constexpr int kTm = kBar + kNumBars * 8;
+    static constexpr int kStage = kKv + kSlots * kTile;    // outputs on their way: 4 KB per softmax warp
+    static constexpr int kBar = kStage + 8 * 4096;
+    static constexpr int kItems = kBar + 48 * 8;           // the blocks being worked on
+    static constexpr int kNext = kItems + 2 * 48;          // the launch control's answers
+    static constexpr int kTm = kNext + 2 * 16;
     static constexpr int kBytes = kTm + 16 + 1024;
     // TMEM columns: two score tiles, two outputs
     static constexpr uint32_t kS = 0, kO = 256;
@@ -242,6 +245,19 @@ __device__ __noinline__ uint4 add_bad_values(const AttnArgs& a, uint4 out, int b
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// One block of work: 2 x span tokens of one sequence, for one key/value head.
+struct Item {
+    int first, len;                                        // the sequence's first row and its length
+    int t0, hk;                                            // first token, within the sequence; key/value head
+    int nk0, nk1, masked;                                  // key tiles of the two query tiles; the first that reaches past some row's diagonal
+    int bad;                                               // masked tiles (from `masked`) with values that are not finite
+    int live;                                              // 0: no more work
+};
+
+// A CTA takes a block of work for its own number and then, one by one, blocks whose CTAs have not
+// been launched yet (cluster launch control cancels their launch and hands over their numbers):
+// the work stays balanced by the hardware, while the next block's loads and first scores run
+// behind the current one's end.
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_prefill_tc_kernel(const __grid_constant__ AttnMaps maps, const __grid_constant__ AttnArgs a, int group, int span, const Divisor block_div,
@@ -251,59 +267,35 @@ attn_prefill_tc_kernel(const __grid_constant__ AttnMaps maps, const __grid_const
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::kBar);
-    uint64_t *q_full = bars, *full = bars + 1, *empty = full + L::kSlots, *s_full = empty + L::kSlots,
-             *p_full = s_full + 2, *o_full = p_full + 4, *v_in = o_full + 2, *v_ok = v_in + kMaxMasked;
+    uint64_t *item_full = bars, *item_empty = bars + 2, *q_empty = bars + 4, *next_full = bars + 5, *s_full = bars + 6,
+             *p_full = bars + 8, *o_full = bars + 12, *o_free = bars + 14, *v_in = bars + 16, *v_ok = v_in + 2 * kMaxMasked,
+             *full = bars + kFixedBars, *empty = full + L::kSlots;
+    static_assert(kFixedBars + 2 * L::kSlots <= 48, "barriers");
+    Item* items = reinterpret_cast<Item*>(sm + L::kItems);
     uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + L::kTm);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L::kTm + 4);
-    int* bad_tiles = reinterpret_cast<int*>(sm + L::kTm + 8);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-    // barriers and TMEM while the offsets are on their way
     if (warp == kWarpTma) {
         if (lane < 3) prefetch_tensor_map(lane == 0 ? &maps.q : lane == 1 ? &maps.k : &maps.v);
-        static_assert(L::kNumBars <= 32, "a lane per barrier");
-        // arrivals per phase: two for the slots' release (a thread per query tile), a tile's rows for P
-        const int e = lane - (1 + L::kSlots), p = lane - (1 + 2 * L::kSlots + 2);
-        if (lane < L::kNumBars) mbar_init(&bars[lane], e >= 0 && e < L::kSlots ? 2 : p >= 0 && p < 4 ? kRows : 1);
-        if (lane == 0) {
-            *abort_flag = 0;
-            *bad_tiles = 0;
-        }
+        // arrivals per phase: an item's 8 softmax warps, 2 issuing threads and the values warp; a
+        // tile's rows for P and for O's release; a thread per query tile for the loads' release
+        for (int i = lane; i < kFixedBars + 2 * L::kSlots; i += 32)
+            mbar_init(&bars[i], i == 2 || i == 3 ? 11 : i == 4 ? 2 : (i >= 8 && i < 12) || i == 14 || i == 15 ? kRows
+                                : i >= kFixedBars + L::kSlots ? 2 : 1);
+        if (lane == 0) *abort_flag = 0;
         fence_mbar_init();
     }
     if (warp == kWarpMma) {
         tmem_alloc(tslot, 512);
         tmem_relinquish();
     }
-
-    // this CTA's rows: blocks with the most keys first, the key/value heads side by side
-    // (group: query heads per key/value head; span: tokens per query tile)
-    const int place = gridDim.x - 1 - blockIdx.x, blk = hkv_div.d > 1 ? hkv_div.div(place) : place, hk = place - blk * a.hkv;
     if (blockIdx.x == 0) check_offsets(a.cu, a.nseq, a.total, err);
-    int seq, j0, first, len;
-    const bool valid = packed_block(a.cu, a.nseq, a.total, block_div, blk, err, &seq, &j0, &first, &len);
-    const int t0 = valid ? j0 * 2 * span : 0;              // first token, within the sequence
-    const bool work = valid && t0 < len;
-    // key tiles that each query tile needs; from `masked` on a tile reaches past some row's diagonal
-    const int nk0 = work ? (min(t0 + span, len) - 1) / kKeys + 1 : 0;
-    const int nk1 = work && t0 + span < len ? (min(t0 + 2 * span, len) - 1) / kKeys + 1 : 0;
-    const int nk = max(nk0, nk1), masked = (t0 + 1) / kKeys;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    auto kv = [&](int n) { return sm + L::kKv + (n % L::kSlots) * L::kTile; };   // K_i is tile 2 i, V_i tile 2 i + 1
-    auto load = [&](int n) {
-        // a masked tile's values go to the values warp first: its barriers are used once, so that
-        // it need not follow the slots' phases (`full` then only marks the turn)
-        uint64_t* slot = &full[n % L::kSlots];
-        const bool to_fix = (n & 1) && (n >> 1) >= masked;
-        uint64_t* bar = to_fix ? &v_in[(n >> 1) - masked] : slot;
-        mbar_expect_tx(bar, L::kTile);
-        for (int h = 0; h < L::kHalves; ++h)
-            tma_load_3d(kv(n) + h * kHalf, n & 1 ? &maps.v : &maps.k, 64 * h, hk, first + (n >> 1) * kKeys, bar);
-        if (to_fix) mbar_arrive(slot);
-    };
     const uint32_t tmem = *tslot;
+    auto kv = [&](int n) { return sm + L::kKv + (n % L::kSlots) * L::kTile; };   // tiles in the order of their loads: K_0 V_0 K_1 ..
     auto wait = [&](uint64_t* bar, int phase) { return mbar_wait_compact(bar, phase & 1, err, abort_flag); };
     auto poll = [&](uint64_t* bar, int phase) { return mbar_wait_compact<true>(bar, phase & 1, err, abort_flag); };
 
@@ -312,17 +304,70 @@ attn_prefill_tc_kernel(const __grid_constant__ AttnMaps maps, const __grid_const
     if (warp >= kWarpTma) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == kWarpTma) {
-        if (elect_one() && nk > 0) {
-            const int tiles = nk1 > 0 ? 2 : 1;
-            mbar_expect_tx(q_full, tiles * L::kHalves * 128 * group * span);
+        // ---------------------------------------------------------------- blocks of work, and their loads
+        const bool leader = elect_one();
+        uint4* next = reinterpret_cast<uint4*>(sm + L::kNext);
+        int cta = blockIdx.x, it = 0, n = 0;
+        bool ok = true;
 #pragma unroll 1
-            for (int j = 0; j < tiles; ++j)
-                for (int h = 0; h < L::kHalves; ++h)
-                    tma_load_3d(sm + j * L::kTile + h * kHalf, &maps.q, 64 * h, hk * group, first + t0 + j * span, q_full);
+        for (int asked = 0; cta >= 0 && ok; ++asked) {
+            // blocks with the most keys first, the key/value heads side by side
+            const int place = gridDim.x - 1 - cta, blk = hkv_div.d > 1 ? hkv_div.div(place) : place, hk = place - blk * a.hkv;
+            int seq, j0, first, len;
+            const bool valid = packed_block(a.cu, a.nseq, a.total, block_div, blk, err, &seq, &j0, &first, &len);
+            const int t0 = valid ? j0 * 2 * span : 0;
+            if (valid && t0 < len) {
+                const int nk0 = (min(t0 + span, len) - 1) / kKeys + 1;
+                const int nk1 = t0 + span < len ? (min(t0 + 2 * span, len) - 1) / kKeys + 1 : 0;
+                const int nk = max(nk0, nk1), masked = (t0 + 1) / kKeys, slot = it & 1;
+                ok = __all_sync(0xffffffffu, (it < 2 || wait(&item_empty[slot], it / 2 - 1)) && (it < 1 || wait(q_empty, it - 1)));
+                if (ok && leader) {
+                    items[slot] = Item{first, len, t0, hk, nk0, nk1, masked, 0, 1};
+                    const int tiles = nk1 > 0 ? 2 : 1;
+                    mbar_expect_tx(&item_full[slot], tiles * L::kHalves * 128 * group * span);
 #pragma unroll 1
-            for (int n = 0; n < 2 * nk; ++n) {
-                if (n >= L::kSlots && !wait(&empty[n % L::kSlots], n / L::kSlots - 1)) break;
-                load(n);
+                    for (int j = 0; j < tiles; ++j)
+                        for (int h = 0; h < L::kHalves; ++h)
+                            tma_load_3d(sm + j * L::kTile + h * kHalf, &maps.q, 64 * h, hk * group, first + t0 + j * span, &item_full[slot]);
+#pragma unroll 1
+                    for (int k = 0; k < 2 * nk; ++k, ++n) {
+                        uint64_t* turn = &full[n % L::kSlots];
+                        if (n >= L::kSlots && !wait(&empty[n % L::kSlots], n / L::kSlots - 1)) {
+                            ok = false;
+                            break;
+                        }
+                        // a masked tile's values go to the values warp first, on barriers of their own, so
+                        // that it need not follow the slots' phases (`full` then only marks the turn)
+                        const bool to_fix = (k & 1) && (k >> 1) >= masked;
+                        uint64_t* bar = to_fix ? &v_in[slot * kMaxMasked + (k >> 1) - masked] : turn;
+                        mbar_expect_tx(bar, L::kTile);
+                        for (int h = 0; h < L::kHalves; ++h)
+                            tma_load_3d(kv(n) + h * kHalf, k & 1 ? &maps.v : &maps.k, 64 * h, hk, first + (k >> 1) * kKeys, bar);
+                        if (to_fix) mbar_arrive(turn);
+                    }
+                }
+                ok = __all_sync(0xffffffffu, ok);
+                ++it;
+            }
+            if (!ok) break;
+            // (asked for only now, with this block's loads under way: a block held in reserve any longer
+            // would be missing where a CTA has run out of work)
+            if (leader) {
+                mbar_expect_tx(next_full, 16);
+                launch_control_next(&next[asked & 1], next_full);
+            }
+            ok = __all_sync(0xffffffffu, wait(next_full, asked)) && ok;
+            cta = ok ? launch_control_cta(next[asked & 1]) : -1;
+        }
+        // the end, as a block of its own (its place is free once the roles are done with what it held)
+        const int slot = it & 1;
+        ok = ok && __all_sync(0xffffffffu, it < 2 || wait(&item_empty[slot], it / 2 - 1));
+        if (!ok)                                           // a wait expired: copies in flight land before the CTA ends
+            for (int i = 0; i < 1000; ++i) __nanosleep(1000);
+        if (ok) {
+            if (leader) {
+                items[slot].live = 0;
+                mbar_arrive(&item_full[slot]);
             }
         }
     } else if (warp == kWarpMma || warp == kWarpMma + 1) {
@@ -331,137 +376,193 @@ attn_prefill_tc_kernel(const __grid_constant__ AttnMaps maps, const __grid_const
         if (elect_one()) {
             constexpr uint32_t idS = idesc_bf16_f32(128, kKeys, false, false);
             constexpr uint32_t idO = idesc_bf16_f32(128, D, false, true);
-            const int j = warp - kWarpMma, own = j ? nk1 : nk0;
+            const int j = warp - kWarpMma;
             const uint32_t tS = tmem + L::kS + j * 128, tO = tmem + L::kO + j * 128;
             const uint64_t dQ = smem_desc_sw128(smem_u32(sm + j * L::kTile), 16, 1024);
-            bool ok = own == 0 || poll(q_full, 0);
+            int n = 0, scores = 0, outputs = 0;            // loads, score tiles and outputs so far
+            uint32_t fixed = 0;                            // phase of each masked tile's barrier
+            bool ok = true;
 #pragma unroll 1
-            for (int i = -1; i < nk && ok; ++i) {
-                // V_i and K_(i+1), waited for before P_i is
-                const int nV = 2 * i + 1, nK = 2 * i + 2;
-                const bool has_v = i >= 0, has_k = i + 1 < nk;
-                if (has_v) ok = poll(&full[nV % L::kSlots], nV / L::kSlots);
-                if (has_k) ok = ok && poll(&full[nK % L::kSlots], nK / L::kSlots);
-                const uint64_t dK = smem_desc_sw128(smem_u32(kv(nK)), 16, 1024);
-                const uint64_t dV = smem_desc_sw128(smem_u32(kv(nV)), kHalf, 1024);
-                if (has_v && i < own) {                    // O += P V_i, P in two parts of 64 keys
-                    if (i >= masked) ok = ok && poll(&v_ok[i - masked], 0);
+            for (int it = 0; ok; ++it) {
+                ok = poll(&item_full[it & 1], it / 2);
+                if (!ok || !items[it & 1].live) break;
+                const Item& x = items[it & 1];
+                const int nk = max(x.nk0, x.nk1), own = j ? x.nk1 : x.nk0, masked = x.masked;
+                if (own == 0) mbar_arrive(q_empty);
 #pragma unroll 1
-                    for (int part = 0; part < 2; ++part) {
-                        ok = ok && poll(&p_full[2 * j + part], i);
-                        if (!ok) break;
+                for (int i = -1; i < nk && ok; ++i) {
+                    // V_i and K_(i+1), waited for before P_i is
+                    const int nV = n + 2 * i + 1, nK = nV + 1;
+                    const bool has_v = i >= 0, has_k = i + 1 < nk;
+                    if (has_v) ok = poll(&full[nV % L::kSlots], nV / L::kSlots);
+                    if (has_k) ok = ok && poll(&full[nK % L::kSlots], nK / L::kSlots);
+                    if (has_v && i >= masked) {            // (by both threads, so that neither misses a phase)
+                        const int k = (it & 1) * kMaxMasked + i - masked;
+                        ok = ok && poll(&v_ok[k], fixed >> k);
+                        fixed ^= 1u << k;
+                    }
+                    const uint64_t dK = smem_desc_sw128(smem_u32(kv(nK)), 16, 1024);
+                    const uint64_t dV = smem_desc_sw128(smem_u32(kv(has_v ? nV : nK)), kHalf, 1024);
+                    if (has_v && i < own) {                // O += P V_i, P in two parts of 64 keys
+                        // (the block before's outputs have been read)
+                        if (i == 0 && outputs > 0) ok = ok && poll(&o_free[j], outputs - 1);
+#pragma unroll 1
+                        for (int part = 0; part < 2; ++part) {
+                            ok = ok && poll(&p_full[2 * j + part], scores);
+                            if (!ok) break;
+                            tc_fence_after();
+#pragma unroll
+                            for (int ks = 0; ks < kKeys / 32; ++ks)
+                                umma_f16_ts(tO, tS + part * 32 + ks * 8, desc_advance(dV, part * 8192 + ks * 2048), idO,
+                                            (i > 0 || part > 0 || ks > 0) ? 1u : 0u);
+                        }
+                        ++scores;
+                    }
+                    if (!ok) break;
+                    if (i + 1 < own) {                     // S = Q K_(i+1)^T
+                        // S over P: products of one thread run in the order of issue, so the one that
+                        // reads P is done with it
                         tc_fence_after();
 #pragma unroll
-                        for (int ks = 0; ks < kKeys / 32; ++ks)
-                            umma_f16_ts(tO, tS + part * 32 + ks * 8, desc_advance(dV, part * 8192 + ks * 2048), idO,
-                                        (i > 0 || part > 0 || ks > 0) ? 1u : 0u);
+                        for (int ks = 0; ks < D / 16; ++ks) {
+                            const uint32_t off = (ks >> 2) * kHalf + (ks & 3) * 32;
+                            umma_f16(tS, desc_advance(dQ, off), desc_advance(dK, off), idS, ks > 0 ? 1u : 0u);
+                        }
+                        umma_commit(&s_full[j]);
+                        if (i + 2 == own) umma_commit(q_empty);
                     }
+                    if (has_v) umma_commit(&empty[nV % L::kSlots]);
+                    if (has_k) umma_commit(&empty[nK % L::kSlots]);
+                    if (has_v && i == own - 1) umma_commit(&o_full[j]);
                 }
-                if (!ok) break;
-                if (i + 1 < own) {                         // S = Q K_(i+1)^T
-                    // S over P: products of one thread run in the order of issue, so the one that
-                    // reads P is done with it
-                    if (i < 0) tc_fence_after();
-#pragma unroll
-                    for (int ks = 0; ks < D / 16; ++ks) {
-                        const uint32_t off = (ks >> 2) * kHalf + (ks & 3) * 32;
-                        umma_f16(tS, desc_advance(dQ, off), desc_advance(dK, off), idS, ks > 0 ? 1u : 0u);
-                    }
-                    umma_commit(&s_full[j]);
-                }
-                if (i == own - 1 && own > 0) umma_commit(o_full + j);
-                if (has_v) umma_commit(&empty[nV % L::kSlots]);
-                if (has_k) umma_commit(&empty[nK % L::kSlots]);
+                n += 2 * nk;
+                if (own > 0) ++outputs;
+                mbar_arrive(&item_empty[it & 1]);
             }
             // no TMEM is released with products in flight
-            if (ok && own > 0) wait(&o_full[j], 0);
+            if (outputs > 0) wait(&o_full[j], outputs - 1);
         }
-    } else if (warp == kWarpValues) {
-        for (int i = masked; i < nk; ++i) {
-            if (!wait(&v_in[i - masked], 0)) break;
-            const bool bad = fix_values<D>(kv(2 * i + 1), min(kKeys, len - i * kKeys), lane);
-            if (bad && lane == 0) atomicOr(bad_tiles, 1 << (i - masked));
-            fence_proxy_async_smem();
+    } else {
+        // ---------------------------------------------------------------- values of masked tiles
+        int n = 0;
+        uint32_t fixed = 0;                                // phase of each masked tile's barrier
+#pragma unroll 1
+        for (int it = 0;; ++it) {
+            if (!__all_sync(0xffffffffu, wait(&item_full[it & 1], it / 2)) || !items[it & 1].live) break;
+            Item* x = &items[it & 1];
+            const int nk = max(x->nk0, x->nk1), masked = x->masked, len = x->len;
+            bool ok = true;
+#pragma unroll 1
+            for (int i = masked; i < nk && ok; ++i) {
+                const int k = (it & 1) * kMaxMasked + i - masked;
+                ok = __all_sync(0xffffffffu, wait(&v_in[k], fixed >> k));
+                if (!ok) break;
+                fixed ^= 1u << k;
+                const bool bad = fix_values<D>(kv(n + 2 * i + 1), min(kKeys, len - i * kKeys), lane);
+                if (bad && lane == 0) x->bad |= 1 << (i - masked);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&v_ok[k]);
+            }
+            if (!ok) break;
+            n += 2 * nk;
             __syncwarp();
-            if (lane == 0) mbar_arrive(&v_ok[i - masked]);
+            if (lane == 0) mbar_arrive(&item_empty[it & 1]);
         }
     }
     } else {
         // ---------------------------------------------------------------- softmax
         asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         const int j = warp >> 2, r = tid & 127;            // query tile, row
-        const int tok = r / group, t = t0 + j * span + tok;   // the row's token, within the sequence
-        const bool live = tok < span && t < len;
-        const int n_own = j ? nk1 : nk0;
+        const int tok = r / group;                         // the row's token, within the tile
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + lanes + L::kS + j * 128, tO = tmem + lanes + L::kO + j * 128;
         const float c = a.scale * kLog2e;
         const bool positive = c > 0.f;
-        float m = __int_as_float(0xff800000), l = 0.f;
+        uint8_t* stage = sm + L::kStage + warp * 4096;
+        int scores = 0, outputs = 0;                       // score tiles and outputs so far
+        // A warp that gives up a wait does no more work but goes on taking its turns, block by
+        // block, so that the other tile's warps are not left at a named barrier; for the same reason
+        // the wait for a block does not end early when another wait has expired.
         bool ok = true;
-        // turns at the exponentials: tile 0 first, then 1, .. while both have key tiles left.  (A
-        // thread that gives up a wait still takes its turns.)
-        if (j == 1 && nk1 > 0) named_bar_arrive(1, 2 * kRows);
-        for (int i = 0; i < n_own; ++i) {
-            const int turn = nk1 > 0 && i < nk0 ? 1 + j : 0;
-            const int next = nk1 > 0 && (j == 0 || i + 1 < nk0) ? 2 - j : 0;
-            ok = ok && __all_sync(0xffffffffu, wait(&s_full[j], i));
-            if (!ok) {
-                if (turn) named_bar_sync(turn, 2 * kRows);
-                if (next) named_bar_arrive(next, 2 * kRows);
-                continue;
-            }
-            tc_fence_after();
-            // (a scale that is not positive is applied before the maximum)
-            if (i >= masked || !positive) prepare_scores(tS, positive ? 1.f : c, !positive, i < masked ? kKeys : t - i * kKeys);
-            row_tile<D>(tS, tO, i > 0, positive ? c : 1.f, m, l, &p_full[2 * j], turn, next);
-        }
-        if (ok && n_own > 0 && __all_sync(0xffffffffu, wait(&o_full[j], 0))) {
-            tc_fence_after();
-            const float inv = 1.f / l;
-            const int bad = *bad_tiles;
-            // a row per thread goes through the query tile's memory (its products have completed), so
-            // that the global stores are whole rows: 16-byte chunks, permuted by the row
-            constexpr int kChunks = D / 8;
-            uint8_t* stage = sm + j * L::kTile + (warp & 3) * 32 * D * 2;
-#pragma unroll 1                                           // (code that runs once comes from far: loops, not copies)
-            for (int q = 0; q < D / 32; ++q) {
-                uint32_t o[32];
-                tmem_ld32(tO + 32 * q, o);
-                tmem_wait_ld();
-                float y[32];
-#pragma unroll
-                for (int e = 0; e < 32; ++e) y[e] = __uint_as_float(o[e]) * inv;
-#pragma unroll
-                for (int e = 0; e < 32; e += 8)
-                    *reinterpret_cast<uint4*>(stage + lane * (D * 2) + (((4 * q + e / 8) ^ (lane & 7)) << 4)) =
-                        make_uint4(pack_bf16x2(y[e], y[e + 1]), pack_bf16x2(y[e + 2], y[e + 3]),
-                                   pack_bf16x2(y[e + 4], y[e + 5]), pack_bf16x2(y[e + 6], y[e + 7]));
-            }
-            __syncwarp();
-            // rows of the tile start at this (token, head); a row's place after it fits 32 bits
-            // (128 tokens of 65535 heads of 128)
-            const int to_row = live ? tok * a.hq + (r - tok * group) : -1;
-            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) +
-                                 ((size_t)(first + t0 + j * span) * a.hq + (size_t)hk * group) * a.dim;
-            if (bad) {
-                // (rare: the staged rows are corrected where they lie)
 #pragma unroll 1
-                for (int c8 = 0; 8 * c8 < a.dim; ++c8) {
-                    uint4* p = reinterpret_cast<uint4*>(stage + lane * (D * 2) + ((c8 ^ (lane & 7)) << 4));
-                    if (live) *p = add_bad_values(a, *p, bad, masked, first, t, hk, 8 * c8);
+        for (int it = 0;; ++it) {
+            if (!__all_sync(0xffffffffu, mbar_wait(&item_full[it & 1], (it / 2) & 1, err)) || !items[it & 1].live) break;
+            const Item* x = &items[it & 1];
+            const int nk0 = x->nk0, nk1 = x->nk1, masked = x->masked, n_own = j ? nk1 : nk0;
+            const int t = x->t0 + j * span + tok;          // the row's token, within the sequence
+            const bool live = tok < span && t < x->len;
+            float m = kNone, l = 0.f;
+            // turns at the exponentials: tile 0 first, then 1, .. while both have key tiles left
+            if (j == 1 && nk1 > 0) named_bar_arrive(1, 2 * kRows);
+#pragma unroll 1
+            for (int i = 0; i < n_own; ++i) {
+                const int turn = nk1 > 0 && i < nk0 ? 1 + j : 0;
+                const int next = nk1 > 0 && (j == 0 || i + 1 < nk0) ? 2 - j : 0;
+                ok = ok && __all_sync(0xffffffffu, wait(&s_full[j], scores));
+                ++scores;
+                if (!ok) {
+                    if (turn) named_bar_sync(turn, 2 * kRows);
+                    if (next) named_bar_arrive(next, 2 * kRows);
+                    continue;
                 }
-                __syncwarp();
+                tc_fence_after();
+                // (a scale that is not positive is applied before the maximum)
+                if (i >= masked || !positive) prepare_scores(tS, positive ? 1.f : c, !positive, i < masked ? kKeys : t - i * kKeys);
+                row_tile<D>(tS, tO, i > 0, positive ? c : 1.f, m, l, &p_full[2 * j], turn, next);
             }
-            const int row0 = lane / kChunks, ch = lane % kChunks;
-            const bool inside = 8 * ch < a.dim;
-            out += 8 * ch;
+            if (n_own > 0) ok = ok && __all_sync(0xffffffffu, wait(&o_full[j], outputs++));
+            if (n_own > 0 && ok) {
+                tc_fence_after();
+                const float inv = 1.f / l;
+                const int bad = x->bad, first = x->first, hk = x->hk;
+                // rows of the tile start at this (token, head); a row's place after it fits 32 bits
+                // (128 tokens of 65535 heads of 128)
+                const int to_row = live ? tok * a.hq + (r - tok * group) : -1;
+                __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) +
+                                     ((size_t)(first + x->t0 + j * span) * a.hq + (size_t)hk * group) * a.dim + 8 * (lane & 7);
+                // 64 dimensions at a time go through shared memory, a row per thread, so that the global
+                // stores are whole rows; 16-byte chunks are permuted by the row
+#pragma unroll 1
+                for (int h = 0; h < L::kHalves; ++h) {
+#pragma unroll 1
+                    for (int q = 0; q < 2; ++q) {
+                        uint32_t o[32];
+                        tmem_ld32(tO + 64 * h + 32 * q, o);
+                        tmem_wait_ld();
+                        float y[32];
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) y[e] = __uint_as_float(o[e]) * inv;
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8)
+                            *reinterpret_cast<uint4*>(stage + lane * 128 + (((4 * q + e / 8) ^ (lane & 7)) << 4)) =
+                                make_uint4(pack_bf16x2(y[e], y[e + 1]), pack_bf16x2(y[e + 2], y[e + 3]),
+                                           pack_bf16x2(y[e + 4], y[e + 5]), pack_bf16x2(y[e + 6], y[e + 7]));
+                    }
+                    if (h == L::kHalves - 1) {             // O may be replaced
+                        tc_fence_before();
+                        mbar_arrive(&o_free[j]);
+                    }
+                    if (bad) {
+                        // (rare: the staged rows are corrected where they lie)
+#pragma unroll 1
+                        for (int c8 = 0; c8 < 8 && 64 * h + 8 * c8 < a.dim; ++c8) {
+                            uint4* p = reinterpret_cast<uint4*>(stage + lane * 128 + ((c8 ^ (lane & 7)) << 4));
+                            if (live) *p = add_bad_values(a, *p, bad, masked, first, t, hk, 64 * h + 8 * c8);
+                        }
+                    }
+                    __syncwarp();
+                    const bool inside = 64 * h + 8 * (lane & 7) < a.dim;
 #pragma unroll 2
-            for (int k = 0; k < kChunks; ++k) {
-                const int row = k * (32 / kChunks) + row0, to = __shfl_sync(0xffffffffu, to_row, row);
-                const uint4 v = *reinterpret_cast<const uint4*>(stage + row * (D * 2) + ((ch ^ (row & 7)) << 4));
-                if (to >= 0 && inside) *reinterpret_cast<uint4*>(out + (size_t)(unsigned)(to * a.dim)) = v;
+                    for (int k = 0; k < 8; ++k) {
+                        const int row = 4 * k + (lane >> 3), to = __shfl_sync(0xffffffffu, to_row, row);
+                        const uint4 v = *reinterpret_cast<const uint4*>(stage + row * 128 + (((lane & 7) ^ (row & 7)) << 4));
+                        if (to >= 0 && inside) *reinterpret_cast<uint4*>(out + 64 * h + (size_t)(unsigned)(to * a.dim)) = v;
+                    }
+                    __syncwarp();
+                }
             }
+            if (lane == 0) mbar_arrive(&item_empty[it & 1]);
         }
     }
     tc_fence_before();

@@ -107,6 +107,26 @@ __device__ __forceinline__ void griddep_wait() {
     asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+// ---------------------------------------------------------------- cluster launch control
+// Asks for the number of a CTA of this grid that has not been launched yet, whose launch is then
+// cancelled: 16 bytes at `answer` (16-byte aligned shared memory), completing on `bar`.
+__device__ __forceinline__ void launch_control_next(void* answer, uint64_t* bar) {
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];"
+                 ::"r"(smem_u32(answer)), "r"(smem_u32(bar)) : "memory");
+}
+// The CTA's number (x) in an answer, -1 when there was none left.
+__device__ __forceinline__ int launch_control_cta(const uint4& answer) {
+    int x;
+    asm volatile(
+        "{\n\t.reg .b128 h;\n\t.reg .b64 lo, hi;\n\t.reg .pred p;\n\t.reg .b32 y, z, w;\n\t"
+        "mov.b64 lo, {%1, %2};\n\tmov.b64 hi, {%3, %4};\n\tmov.b128 h, {lo, hi};\n\t"
+        "mov.b32 %0, -1;\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%0, y, z, w}, h;\n\t}"
+        : "=&r"(x) : "r"(answer.x), "r"(answer.y), "r"(answer.z), "r"(answer.w));
+    return x;
+}
+
 // ---------------------------------------------------------------- named barriers
 __device__ __forceinline__ void named_bar_sync(uint32_t id, uint32_t nthreads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");

@@ -54,6 +54,15 @@ def test_long_prompt_with_neighbours(dtype, hq, hkv, dim):
 
 
 @pytest.mark.parametrize("dtype", [bf, f32])
+@pytest.mark.parametrize("hq,hkv,dim", [(8, 8, 128), (12, 4, 64), (16, 8, 40)])
+def test_many_short_sequences(dtype, hq, hkv, dim):
+    """More blocks of work than run at a time, several times over, with empty sequences between them
+    and now and then a sequence of several blocks."""
+    lens = [(37 * i) % 130 if i % 31 else 400 for i in range(230)]
+    check(lens, *problem(sum(lens), hq, hkv, dim, dtype, seed=31), dim ** -0.5, f"{hq}/{hkv} heads of {dim}")
+
+
+@pytest.mark.parametrize("dtype", [bf, f32])
 @pytest.mark.parametrize("scale", [0.0, -0.3, 4.0])
 def test_scales(dtype, scale):
     """Uniform weights, a negative scale, and one whose softmax is nearly one key."""
