@@ -221,7 +221,7 @@ linattn_scan_kernel(const LinattnArgs a, float* states)
 
 template <typename T, int DK, int DV>
 __global__ void __launch_bounds__(kThreads)
-linattn_block_output_kernel(const LinattnArgs a, const Divisor block, const float* __restrict__ states, int* err)
+linattn_block_output_kernel(const LinattnArgs a, const Divisor block, const float* states, int* err)
 {
     constexpr int kLdK = DK + 4, kLdV = DV + 4, kC = DV / 64;
     extern __shared__ float sm[];

@@ -809,7 +809,8 @@ bool make_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, u
 // Tiled map of `rank` dimensions (dim 0 contiguous; strides in bytes for dims 1..rank-1),
 // 128-byte swizzle or none; out-of-range elements read as zero.
 bool encode_map(CUtensorMap* m, CUtensorMapDataType type, int rank, const void* base,
-                const uint64_t* dims, const uint64_t* strides, const uint32_t* box, bool swizzle)
+                const uint64_t* dims, const uint64_t* strides, const uint32_t* box, bool swizzle,
+                CUtensorMapL2promotion promotion = CU_TENSOR_MAP_L2_PROMOTION_L2_256B)
 {
     auto fn = encode_fn();
     if (!fn) return false;
@@ -823,7 +824,7 @@ bool encode_map(CUtensorMap* m, CUtensorMapDataType type, int rank, const void* 
     }
     return fn(m, type, rank, const_cast<void*>(base), gd, gs, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
               swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+              promotion, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 int sm_count();
@@ -922,9 +923,10 @@ bool tc_make_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows
 int tc_sm_count() { return sm_count(); }
 
 bool tc_encode_map(CUtensorMap* m, CUtensorMapDataType type, int rank, const void* base,
-                   const uint64_t* dims, const uint64_t* strides, const uint32_t* box, bool swizzle)
+                   const uint64_t* dims, const uint64_t* strides, const uint32_t* box, bool swizzle,
+                   CUtensorMapL2promotion promotion)
 {
-    return encode_map(m, type, rank, base, dims, strides, box, swizzle);
+    return encode_map(m, type, rank, base, dims, strides, box, swizzle, promotion);
 }
 
 bool tc_prefill_supported(const Dims& d)

@@ -77,7 +77,8 @@ bool tc_make_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows
 // Tiled map of `rank` dimensions (dim 0 contiguous, strides in bytes for dims 1..rank-1),
 // 128-byte swizzle or none.
 bool tc_encode_map(CUtensorMap* m, CUtensorMapDataType type, int rank, const void* base,
-                   const uint64_t* dims, const uint64_t* strides, const uint32_t* box, bool swizzle);
+                   const uint64_t* dims, const uint64_t* strides, const uint32_t* box, bool swizzle,
+                   CUtensorMapL2promotion promotion = CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 int tc_sm_count();
 
 // Launch with programmatic stream serialisation: the kernel may start while the previous

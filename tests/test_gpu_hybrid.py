@@ -1,0 +1,171 @@
+"""The mixers together, as a hybrid model runs them: a stack of a state-space, a linear-attention and
+an attention layer takes packed prompts, keeps its states and caches, and goes on one token at a time,
+step by step and as captured graphs that share a workspace.  Every call's outputs are checked against
+fp64 on the inputs that the stack gave it, which follow from the layers before it."""
+import pytest
+import torch
+
+import mixers_ref as ref
+import state_space_model_05_b200 as ssd
+
+pytestmark = pytest.mark.gpu
+
+bf, f32 = torch.bfloat16, torch.float32
+WIDTH, CAPACITY = 128, 320
+HQ, HKV, DIM = 8, 2, 64                            # attention
+LQ, LV, DK, DV = 2, 4, 64, 64                      # linear attention
+SH, SP, SN = 4, 64, 128                            # state space
+
+
+@pytest.fixture(autouse=True, scope="module")
+def _built():
+    from state_space_model_05_b200.build import build
+    build()
+
+
+class Stack:
+    """Two layers of each kind; `seen` keeps what the new calls were given and gave."""
+
+    def __init__(self, dtype, batch):
+        w = lambda rows, cols, seed: (ref.randn(rows, cols, seed=seed) * rows ** -0.5).to(dtype)  # noqa: E731
+        self.dtype, self.layers, self.seen = dtype, [], None
+        for i, kind in enumerate(["ssd", "lin", "attn"] * 2):
+            cols = {"ssd": SH * SP + 2 * SN, "lin": 2 * LQ * DK + LV * DV, "attn": (HQ + 2 * HKV) * DIM}[kind]
+            back = {"ssd": SH * SP, "lin": LV * DV, "attn": HQ * DIM}[kind]
+            layer = dict(kind=kind, win=w(WIDTH, cols, 10 * i), wout=w(back, WIDTH, 10 * i + 1))
+            if kind == "ssd":
+                layer.update(A=-torch.rand(SH, device="cuda") - 0.1, D=torch.ones(SH, device="cuda"),
+                             state=torch.zeros(batch, SH, SP, SN, device="cuda"))
+            elif kind == "lin":
+                layer.update(ld=-0.02 * torch.arange(LV, device="cuda"), state=torch.zeros(batch, LV, DK, DV, device="cuda"))
+            else:
+                layer.update(kc=torch.full((batch, CAPACITY, HKV, DIM), float("nan"), dtype=dtype, device="cuda"),
+                             vc=torch.full((batch, CAPACITY, HKV, DIM), float("nan"), dtype=dtype, device="cuda"))
+            self.layers.append(layer)
+        code = 0 if dtype == f32 else 1
+        self.workspace = torch.empty(ssd.binding.lib().ssd_attn_decode_workspace_bytes(batch, CAPACITY, HQ, HKV, DIM, code),
+                                     dtype=torch.uint8, device="cuda")
+
+    def tensors(self):
+        return [L[n] for L in self.layers for n in ("state", "kc", "vc") if n in L]
+
+    def split(self, layer, x):
+        norm = torch.nn.functional.rms_norm(x.float(), (WIDTH,)).to(self.dtype)
+        p, t = norm @ layer["win"], x.shape[0]
+        if layer["kind"] == "ssd":
+            x, b, c = p.split([SH * SP, SN, SN], 1)
+            return x.reshape(t, SH, SP), b.reshape(t, 1, SN), c.reshape(t, 1, SN)
+        sizes, heads = (([LQ * DK, LQ * DK, LV * DV], (LQ, LQ, LV)) if layer["kind"] == "lin" else
+                        ([HQ * DIM, HKV * DIM, HKV * DIM], (HQ, HKV, HKV)))
+        return [y.unflatten(1, (h, -1)) for y, h in zip(p.split(sizes, 1), heads)]   # slices, not copies
+
+    def dt(self, t):
+        return torch.full((t, SH), 0.1, device="cuda")
+
+    def note(self, *what):
+        if self.seen is not None:
+            self.seen.append(what)
+
+    def prefill(self, x, lens):
+        offsets, cu = ref.offsets(lens), ref.cu(lens)
+        for L in self.layers:
+            q, k, v = self.split(L, x)
+            if L["kind"] == "ssd":
+                q, k, v = (z.contiguous() for z in (q, k, v))
+                y, L["state"] = ssd.ssd_prefill_varlen(q, self.dt(len(x)), L["A"], k, v, L["D"], cu, 128)
+            elif L["kind"] == "lin":
+                y, L["state"] = ssd.ssd_linattn_prefill(q, k, v, L["ld"], cu, scale=DK ** -0.5)
+                self.note("lin", q, k, v, L["ld"], y, L["state"].clone())
+            else:
+                y = ssd.ssd_attn_prefill(q, k, v, cu)
+                for b, n in enumerate(lens):
+                    L["kc"][b, :n], L["vc"][b, :n] = (z[offsets[b]:offsets[b + 1]] for z in (k, v))
+                self.note("attn", q, k, v, y)
+            x = x + y.flatten(1).to(self.dtype) @ L["wout"]
+        return x
+
+    def step(self, x, lens):
+        """lens: cached tokens per row, int32 on the device; advanced."""
+        for L in self.layers:
+            q, k, v = (z.contiguous() for z in self.split(L, x))
+            if L["kind"] == "ssd":
+                y = ssd.ssd_decode_step(L["state"], q, self.dt(len(x)), L["A"], k, v, L["D"])
+            elif L["kind"] == "lin":
+                before = L["state"].clone()
+                y = ssd.ssd_linattn_decode_step(L["state"], q, k, v, L["ld"], scale=DK ** -0.5)
+                self.note("lin", before, q, k, v, L["ld"], y, L["state"].clone())
+            else:
+                y = ssd.ssd_attn_decode_step(L["kc"], L["vc"], lens, q, k, v, workspace=self.workspace)
+                self.note("attn", L["kc"].clone(), L["vc"].clone(), lens.tolist() if self.seen is not None else None, q, k, v, y)
+            x = x + y.flatten(1).to(self.dtype) @ L["wout"]
+        lens += 1
+        return x
+
+
+@pytest.mark.parametrize("dtype", [bf, f32])
+def test_prompts_then_tokens(dtype):
+    lens = [150, 1, 0, 290, 64]
+    stack = Stack(dtype, len(lens))
+    stack.seen = []
+    x = stack.prefill(ref.randn(sum(lens), WIDTH, seed=1, dtype=dtype), lens)
+    assert torch.isfinite(x).all()
+    for kind, q, k, v, *rest in stack.seen:
+        if kind == "lin":
+            wo, wf, to, tf = ref.linattn(q, k, v, rest[0], lens, DK ** -0.5)
+            ref.assert_within(rest[1], wo, to, "linear attention")
+            ref.assert_within(rest[2], wf, tf, "linear attention: states")
+        else:
+            wo, to = ref.attn(q, k, v, lens, DIM ** -0.5)
+            ref.assert_within(rest[0], wo, to, "attention")
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    for i in range(3):
+        stack.seen = []
+        x = stack.step(ref.randn(len(lens), WIDTH, seed=2 + i, dtype=dtype), n)
+        assert torch.isfinite(x).all()
+        for kind, *a in stack.seen:
+            if kind == "lin":
+                before, q, k, v, ld, y, after = a
+                wo, ws, to, ts = ref.linattn_step(before, q, k, v, ld, DK ** -0.5)
+                ref.assert_within(y, wo, to, f"token {i}: linear attention")
+                ref.assert_within(after, ws, ts, f"token {i}: linear attention: states")
+            else:
+                kc, vc, at, q, k, v, y = a
+                wo, to = ref.attn_step(kc, vc, at, q, k, v, DIM ** -0.5)
+                ref.assert_within(y, wo, to, f"token {i}: attention")
+    assert n.tolist() == [m + 3 for m in lens] and ssd.ssd_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", [bf, f32])
+def test_captured_steps_share_a_workspace(dtype):
+    """Two stacks' steps captured as two graphs over one workspace, replayed in turn, equal eager steps."""
+    lens, tokens = [150, 1, 0, 290, 64], 4
+    prompts = [ref.randn(sum(lens), WIDTH, seed=20 + i, dtype=dtype) for i in range(2)]
+    steps = [[ref.randn(len(lens), WIDTH, seed=30 + 10 * i + t, dtype=dtype) for t in range(tokens)] for i in range(2)]
+    stacks = [Stack(dtype, len(lens)) for _ in range(2)]
+    stacks[1].workspace = stacks[0].workspace
+    want, kept, graphs = [], [], []
+    for stack, prompt, xs in zip(stacks, prompts, steps):
+        stack.prefill(prompt, lens)
+        kept.append([z.clone() for z in stack.tensors()])
+        n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+        want.append([stack.step(x, n) for x in xs])
+        want[-1].append([z.clone() for z in stack.tensors()])
+    for stack in stacks:
+        x, n = torch.zeros(len(lens), WIDTH, dtype=dtype, device="cuda"), torch.tensor(lens, dtype=torch.int32, device="cuda")
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            y = stack.step(x, n)
+        graphs.append((graph, x, n, y))
+    for stack, was in zip(stacks, kept):
+        for z, old in zip(stack.tensors(), was):
+            z.copy_(old)
+    for t in range(tokens):
+        for i, (graph, x, _, y) in enumerate(graphs):
+            x.copy_(steps[i][t])
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(y, want[i][t]), f"stack {i}, token {t}"
+    for stack, w in zip(stacks, want):
+        for z, old in zip(stack.tensors(), w[-1]):
+            assert torch.equal(z.nan_to_num(7.0), old.nan_to_num(7.0))
+    assert ssd.ssd_device_status() == 0
