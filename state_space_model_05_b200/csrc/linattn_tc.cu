@@ -150,7 +150,6 @@ linattn_segment_kernel(const __grid_constant__ LinattnMaps maps, const __grid_co
     Powers* pw = reinterpret_cast<Powers*>(sm + L::kPow);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int unit = hv_div.d > 1 ? hv_div.div(blockIdx.x) : (int)blockIdx.x, h = blockIdx.x - unit * a.hv;
-    griddep_launch_dependents();
     Segment sg;
     // the last segment of a sequence hands its state to no one
     if (!this_segment(a, blocks, seg_div, unit, err, &sg) || sg.start + blocks * kBlk >= sg.seq_len) return;
@@ -177,6 +176,9 @@ linattn_segment_kernel(const __grid_constant__ LinattnMaps maps, const __grid_co
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    // (with this kernel's TMEM in hand: a CTA of the output kernel that shares the SM takes all that
+    // is left of it and then waits for this kernel's end)
+    griddep_launch_dependents();
     const uint32_t tmem = *tslot;
     auto wait = [&](uint64_t* bar, int phase) { return mbar_wait_compact(bar, phase & 1, err, abort_flag); };
     auto conv = [&](int n) { return sm + L::kConv + (n % kSegSlots) * kSlot; };
@@ -302,7 +304,7 @@ __device__ __noinline__ float own_sum(const LinattnArgs& a, const Powers* pw, si
 template <int DK, int DV>
 __global__ void __launch_bounds__(kOutThreads, 1)
 linattn_output_kernel(const __grid_constant__ LinattnMaps maps, const __grid_constant__ LinattnArgs a, int blocks, const Divisor seg_div,
-                      const Divisor hv_div, const float4* __restrict__ states, int* err)
+                      const Divisor hv_div, const float4* states, int* err)
 {
     using L = OutCfg<DK, DV>;
     extern __shared__ uint8_t smem_raw[];
@@ -320,7 +322,10 @@ linattn_output_kernel(const __grid_constant__ LinattnMaps maps, const __grid_con
     const int unit = hv_div.d > 1 ? hv_div.div(blockIdx.x) : (int)blockIdx.x, h = blockIdx.x - unit * a.hv;
     if (blockIdx.x == 0) check_offsets(a.cu, a.nseq, a.total, err);
     Segment sg;
-    if (!this_segment(a, blocks, seg_div, unit, err, &sg)) return;
+    if (!this_segment(a, blocks, seg_div, unit, err, &sg)) {
+        griddep_wait();                                    // this grid ends after the one before, here and below
+        return;
+    }
     const int nb = (sg.len + kBlk - 1) / kBlk;             // 0 for an empty sequence
     const int last = sg.len - (nb - 1) * kBlk;             // tokens of the last block
     const bool ends = sg.start + sg.len >= sg.seq_len;     // this segment writes the final state
@@ -715,6 +720,7 @@ linattn_output_kernel(const __grid_constant__ LinattnMaps maps, const __grid_con
     }
     tc_fence_before();
     __syncthreads();
+    griddep_wait();
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
@@ -775,6 +781,9 @@ cudaError_t launch_t(const LinattnArgs& a, float4* states, cudaStream_t s)
     }
     e = cudaFuncSetAttribute(linattn_output_kernel<DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, OutCfg<DK, DV>::kBytes);
     if (e != cudaSuccess) return e;
+    if (a.total > blocks * kBlk)                           // its first segments start while the segment kernel's last ones run
+        return launch_dependent(linattn_output_kernel<DK, DV>, dim3((unsigned)grid), dim3(kOutThreads), OutCfg<DK, DV>::kBytes, s, maps, a,
+                                blocks, seg_div, hv_div, states, err);
     linattn_output_kernel<DK, DV><<<(unsigned)grid, kOutThreads, OutCfg<DK, DV>::kBytes, s>>>(maps, a, blocks, seg_div, hv_div, states, err);
     return cudaGetLastError();
 }
