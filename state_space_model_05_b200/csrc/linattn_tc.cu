@@ -21,6 +21,8 @@
 // rounded to bf16 once, each by at most half the output's own rounding step.
 #include <cuda.h>
 
+#include <cmath>
+
 #include "mixers.cuh"
 #include "prefill_tc.h"
 #include "ptx.cuh"
@@ -728,26 +730,60 @@ linattn_output_kernel(const __grid_constant__ LinattnMaps maps, const __grid_con
 }
 
 // ---------------------------------------------------------------- host side
-// Blocks per segment: the length at which the waves of the two kernels cost least for
-// sequences of average length.  Per 128-token block the output kernel takes about 3 us and the
-// segment kernel 1.6 us when all SMs are busy, either about 4 us to start and end.
+// Blocks per segment: the length that costs least.  Us of a CTA, all SMs busy: a block of 128 tokens
+// 2.5 in the output kernel and 1.75 in the segment kernel, 6 and 2 more to start and end, 1 for a
+// CTA that finds nothing to do, 1 to add a segment's state to the next one's.
+// One sequence: whole waves of equal CTAs.  More: the host knows only their average length and takes
+// the lengths as exponentially spread (a sequence goes on past k segments with probability
+// e^(-k len / avg), the longest of n has avg (ln n + 0.6)); a kernel then takes its work shared
+// evenly and a fifth of its longest CTA, at least that CTA.
+// Measured: 31 sequences cut at random from 16384 tokens, 32 heads: 209 us at the chosen 40 blocks, 270 us at
+// their average of 5; 1024 tokens, 8 heads: 26 us at 1, 39 us at 4; 8192 tokens, 32 heads: 128 us at 16, 194 us
+// at 4; worst found: 30 sequences of up to 300 tokens and one of 4000, 16 heads: 110 us, 100 us at 5.
 int segment_blocks(int nseq, int total, int hv)
 {
-    const long long sms = tc_sm_count();
-    const long long avg = max(1LL, ((long long)total / nseq + kBlk - 1) / kBlk);
-    int best = 4;
-    double best_cost = 0;
-    for (int len = 4; len <= 1024; ++len) {
-        const long long segs = (avg + len - 1) / len, units = segs * nseq * hv, inner = (segs - 1) * nseq * hv;
-        const double cost = (double)((units + sms - 1) / sms) * (3.0 * min((long long)len, avg) + 4.0) +
-                            (double)((inner + sms - 1) / sms) * (1.6 * len + 4.0);
-        if (len == 4 || cost < best_cost) {
-            best = len;
-            best_cost = cost;
+    constexpr double kOut = 2.5, kOutCta = 6, kSeg = 1.75, kSegCta = 2, kIdle = 1, kJoin = 1, kTail = 0.2;
+    const double sms = tc_sm_count();
+    const long long all = max(1LL, ((long long)total + kBlk - 1) / kBlk), avg = max(1LL, ((long long)total / nseq + kBlk - 1) / kBlk);
+    auto cost = [&](long long len) {
+        const double launched = ((double)(total / (kBlk * len)) + nseq) * hv;      // CTAs, of either kernel
+        const bool split = total > len * kBlk;
+        double us;
+        if (nseq == 1) {
+            const double segs = (double)((avg + len - 1) / len);
+            us = std::ceil(segs * hv / sms) * (kOut * min(len, avg) + kOutCta) + (segs - 1) * kJoin;
+            if (split) us += std::ceil((segs - 1) * hv / sms) * (kSeg * len + kSegCta);
+        } else {
+            const double inner = (double)nseq * hv / (std::exp((double)len / avg) - 1), units = (double)nseq * hv + inner;
+            auto even = [&](double work, double longest) { return max(work / sms + kTail * longest, longest); };
+            us = even(all * hv * kOut + units * kOutCta + max(0.0, launched - units) * kIdle,
+                      kOut * min((double)len, avg * (std::log((double)nseq) + 0.6)) + kOutCta) +
+                 (avg + len - 1) / len * kJoin;
+            if (split)
+                us += even(inner * (kSeg * len + kSegCta) + max(0.0, launched - inner) * kIdle, min(1.0, inner / hv) * (kSeg * len + kSegCta));
         }
-        if (len >= avg) break;
+        return us;
+    };
+    long long best = avg;
+    double least = cost(best);
+    auto consider = [&](long long len) {
+        const double us = cost(len);
+        if (us < least) {
+            least = us;
+            best = len;
+        }
+    };
+    // an average sequence in 2, 3, .. equal segments, each length once
+    for (long long len = avg; len > 1;) {
+        const long long segs = (avg + len - 2) / (len - 1);
+        len = (avg + segs - 1) / segs;
+        consider(len);
     }
-    return best;
+    // and segments of several average sequences, while a sequence much longer than the others would
+    // not keep one CTA at work for much longer than an SM's share of all blocks takes
+    for (int m : {2, 3, 4, 6, 8, 12, 16})
+        if (nseq > 1 && (m == 2 || avg * m * sms <= 1.5 * (double)all * hv)) consider(min(all, avg * m));
+    return (int)best;
 }
 
 bool token_map(CUtensorMap* m, const void* p, int dim, int heads, int tokens, long long stride)
