@@ -302,7 +302,8 @@ ssd_status_t ssd_gdn_decode_step(float* state, const void* q, const void* k, con
  *   out    [total_tokens][heads_v][dv] dtype (contiguous), rounded once from fp32.
  * `workspace` holds ssd_linattn_prefill_workspace_bytes(...) bytes of device memory.
  * Requirements: heads_v % heads_qk == 0; dk and dv multiples of 8 up to 128; heads up to
- * 65535; nseq in [1, 2^20]; 16-byte aligned pointers (cu_seqlens: 4).  bf16 runs on the
+ * 65535; nseq in [1, 2^20]; total_tokens up to 2^31 - 1024; no output overlaps an input (the
+ * states excepted); calls that may overlap on the GPU need workspaces of their own; 16-byte aligned pointers (cu_seqlens: 4).  bf16 runs on the
  * tensor cores, fp32 on the CUDA cores.
  */
 size_t ssd_linattn_prefill_workspace_bytes(int nseq, int total_tokens, int heads_qk, int heads_v, int dk,
@@ -333,8 +334,9 @@ ssd_status_t ssd_linattn_decode_step(float* state, const void* q, const void* k,
  *   out [total_tokens][heads_q][headdim] dtype (contiguous), rounded once from fp32.
  * Tokens of one sequence never see another's, whatever values those hold.
  * Requirements: heads_q % heads_kv == 0; headdim a multiple of 8 up to 128; heads up to
- * 65535; nseq in [1, 2^20]; 16-byte aligned pointers (cu_seqlens: 4).  bf16 runs on the
- * tensor cores, fp32 on the CUDA cores.  No workspace.
+ * 65535; nseq in [1, 2^20]; total_tokens up to 2^31 - 1024; `out` overlaps no input; 16-byte
+ * aligned pointers (cu_seqlens: 4).  bf16 runs on the tensor cores (up to 128 query heads per
+ * key/value head), fp32 on the CUDA cores.  No workspace.
  */
 ssd_status_t ssd_attn_prefill(const void* q, const void* k, const void* v, long long q_stride,
                               long long k_stride, long long v_stride, const int* cu_seqlens, int nseq,
@@ -351,7 +353,8 @@ ssd_status_t ssd_attn_prefill(const void* q, const void* k, const void* v, long 
  * attends to rows 0 .. cache_lens[b].  The lengths are not advanced: the caller adds one when
  * every layer has run.  A negative length marks an unused batch row: its caches and its row
  * of `out` are left as they were.  A length of `capacity` or more records SSD_ERR_SHAPE in the
- * device error word, and that row is left as it was.  Cached rows past a length are never read.
+ * device error word, and that row is left as it was.  What cached rows past a length hold plays no
+ * part.  A batch row's caches must not be another's.
  * `workspace` holds ssd_attn_decode_workspace_bytes(...) bytes of device memory; calls that may
  * overlap on the GPU need workspaces of their own.  Results do not depend on the order in which
  * the GPU runs the work.  Requirements as for ssd_attn_prefill; capacity >= 1.

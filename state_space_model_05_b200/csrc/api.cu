@@ -428,9 +428,10 @@ ssd_status_t check_mixer(int rows, int heads_shared, int heads, int dk, int dv, 
     return SSD_OK;
 }
 
-ssd_status_t check_packed(int nseq, long long heads)
+// (block ends past the last token have to fit 32 bits too)
+ssd_status_t check_packed(int nseq, int total, long long heads)
 {
-    return nseq < 1 || nseq > (1 << 20) || nseq * heads > 0x7fffffffLL ? SSD_ERR_SHAPE : SSD_OK;
+    return nseq < 1 || nseq > (1 << 20) || total > 0x7fffffff - 1023 || nseq * heads > 0x7fffffffLL ? SSD_ERR_SHAPE : SSD_OK;
 }
 
 }  // namespace
@@ -438,7 +439,7 @@ ssd_status_t check_packed(int nseq, long long heads)
 size_t ssd_linattn_prefill_workspace_bytes(int nseq, int total_tokens, int heads_qk, int heads_v, int dk,
                                            int dv, ssd_dtype_t dtype)
 {
-    if (check_mixer(total_tokens, heads_qk, heads_v, dk, dv, dtype) != SSD_OK || check_packed(nseq, heads_v) != SSD_OK)
+    if (check_mixer(total_tokens, heads_qk, heads_v, dk, dv, dtype) != SSD_OK || check_packed(nseq, total_tokens, heads_v) != SSD_OK)
         return 0;
     const size_t need = dtype == SSD_BF16 ? linattn_tc_workspace(nseq, total_tokens, heads_v, dk, dv)
                                           : linattn_simt_workspace(nseq, total_tokens, heads_v, dk, dv);
@@ -453,7 +454,7 @@ ssd_status_t ssd_linattn_prefill(const void* q, const void* k, const void* v, lo
                                  size_t workspace_bytes, void* stream)
 {
     ssd_status_t st = check_mixer(total_tokens, heads_qk, heads_v, dk, dv, dtype);
-    if (st == SSD_OK) st = check_packed(nseq, heads_v);
+    if (st == SSD_OK) st = check_packed(nseq, total_tokens, heads_v);
     if (st != SSD_OK) return st;
     if (total_tokens > 0 && (!stride_ok(q_stride, heads_qk, dk) || !stride_ok(k_stride, heads_qk, dk) ||
                              !stride_ok(v_stride, heads_v, dv)))
@@ -495,7 +496,7 @@ ssd_status_t ssd_attn_prefill(const void* q, const void* k, const void* v, long 
                               ssd_dtype_t dtype, void* out, void* stream)
 {
     ssd_status_t st = check_mixer(total_tokens, heads_kv, heads_q, headdim, headdim, dtype);
-    if (st == SSD_OK) st = check_packed(nseq, heads_q);
+    if (st == SSD_OK) st = check_packed(nseq, total_tokens, heads_q);
     if (st != SSD_OK) return st;
     if (total_tokens == 0) return SSD_OK;
     if (!stride_ok(q_stride, heads_q, headdim) || !stride_ok(k_stride, heads_kv, headdim) ||

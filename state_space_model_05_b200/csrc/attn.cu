@@ -56,8 +56,8 @@ attn_prefill_kernel(const AttnArgs a, const Divisor block, int* err)
     int seq, j, first, len;
     // the blocks with the most keys first
     if (!packed_block(a.cu, a.nseq, a.total, block, gridDim.x - 1 - blockIdx.x, err, &seq, &j, &first, &len)) return;
+    if ((long long)j * kRows >= len) return;
     const int q0 = j * kRows, n = min(kRows, len - q0);
-    if (n <= 0) return;
     const size_t t0 = (size_t)first + q0;
     const int hk = h / (a.hq / a.hkv), tiles = (q0 + n - 1) / kKeys + 1;
     load_rows<T, D, kRows>(sq, static_cast<const T*>(a.q) + t0 * a.q_stride + (size_t)h * a.dim, a.q_stride, n, a.dim,

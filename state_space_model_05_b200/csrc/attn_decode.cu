@@ -242,6 +242,7 @@ attn_decode_bf16_kernel(const __grid_constant__ CacheMaps maps, const AttnDecode
                 }
                 cur.next(a.lens, a.capacity, un.per_row, x + 1 < x1);
             }
+            settle(abort_flag);
         }
         return;
     }
@@ -579,8 +580,8 @@ attn_decode_f32_kernel(const AttnDecodeArgs a, float* __restrict__ pieces, int* 
 // head, one thread per dimension, the pieces in the order of their CTAs.  A long row is cut
 // into hundreds of pieces: their weights are formed side by side first, so that the sum's loads
 // do not wait for one another; up to kFew pieces are loaded at once with their maxima and sums
-// (32 rows of up to 4096 positions: 54.5 us -> 52.9 us for both kernels).  (`pieces` is written while this kernel already runs, so it is not
-// declared as read-only.)
+// (32 rows of up to 4096 positions: 54.5 us -> 52.9 us for both kernels).  (`pieces` is written while
+// this kernel already runs, so it is not declared as read-only.)
 constexpr int kFew = 4;
 
 template <typename T, int kUnitRows>

@@ -315,8 +315,8 @@ attn_prefill_tc_kernel(const __grid_constant__ AttnMaps maps, const __grid_const
             const int place = gridDim.x - 1 - cta, blk = hkv_div.d > 1 ? hkv_div.div(place) : place, hk = place - blk * a.hkv;
             int seq, j0, first, len;
             const bool valid = packed_block(a.cu, a.nseq, a.total, block_div, blk, err, &seq, &j0, &first, &len);
-            const int t0 = valid ? j0 * 2 * span : 0;
-            if (valid && t0 < len) {
+            if (valid && (long long)j0 * 2 * span < len) {
+                const int t0 = j0 * 2 * span;
                 const int nk0 = (min(t0 + span, len) - 1) / kKeys + 1;
                 const int nk1 = t0 + span < len ? (min(t0 + 2 * span, len) - 1) / kKeys + 1 : 0;
                 const int nk = max(nk0, nk1), masked = (t0 + 1) / kKeys, slot = it & 1;
@@ -362,8 +362,7 @@ attn_prefill_tc_kernel(const __grid_constant__ AttnMaps maps, const __grid_const
         // the end, as a block of its own (its place is free once the roles are done with what it held)
         const int slot = it & 1;
         ok = ok && __all_sync(0xffffffffu, it < 2 || wait(&item_empty[slot], it / 2 - 1));
-        if (!ok)                                           // a wait expired: copies in flight land before the CTA ends
-            for (int i = 0; i < 1000; ++i) __nanosleep(1000);
+        settle(abort_flag);
         if (ok) {
             if (leader) {
                 items[slot].live = 0;

@@ -132,8 +132,8 @@ linattn_block_state_kernel(const LinattnArgs a, const Divisor block, float* __re
     if (blockIdx.x == 0 && h == 0) check_offsets(a.cu, a.nseq, a.total, err);
     int seq, j, first, len;
     if (!packed_block(a.cu, a.nseq, a.total, block, blockIdx.x, err, &seq, &j, &first, &len)) return;
+    if ((long long)j * kTok >= len) return;
     const int n = min(kTok, len - j * kTok);
-    if (n <= 0) return;
     const size_t t0 = (size_t)first + (size_t)j * kTok;
     if (tid < n) sw[tid] = decay_pow(a.log_decay[h], n - 1 - tid);
     load_rows<T, DK>(sk, static_cast<const T*>(a.k) + t0 * a.k_stride + (size_t)(h / (a.hv / a.hq)) * a.dk, a.k_stride, n, a.dk);
@@ -231,7 +231,7 @@ linattn_block_output_kernel(const LinattnArgs a, const Divisor block, const floa
     const int h = blockIdx.y, tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     int seq, j, first, len;
     const bool valid = packed_block(a.cu, a.nseq, a.total, block, blockIdx.x, err, &seq, &j, &first, &len);
-    const int n = valid ? min(kTok, len - j * kTok) : 0;
+    const int n = valid && (long long)j * kTok < len ? min(kTok, len - j * kTok) : 0;
     if (n <= 0) {
         ptx::griddep_wait();                               // (this grid ends after the one before)
         return;

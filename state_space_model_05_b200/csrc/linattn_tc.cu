@@ -113,8 +113,8 @@ __device__ __forceinline__ bool this_segment(const LinattnArgs& a, int blocks, c
 {
     int first, len;
     if (!packed_block(a.cu, a.nseq, a.total, len_div, unit, err, &s->seq, &s->j, &first, &len)) return false;
+    if (s->j > 0 && (long long)s->j * blocks * kBlk >= len) return false;
     s->start = s->j * blocks * kBlk;
-    if (s->j > 0 && s->start >= len) return false;
     s->seq_len = len;
     s->len = min(blocks * kBlk, len - s->start);
     s->first = first + s->start;
@@ -154,7 +154,7 @@ linattn_segment_kernel(const __grid_constant__ LinattnMaps maps, const __grid_co
     const int unit = hv_div.d > 1 ? hv_div.div(blockIdx.x) : (int)blockIdx.x, h = blockIdx.x - unit * a.hv;
     Segment sg;
     // the last segment of a sequence hands its state to no one
-    if (!this_segment(a, blocks, seg_div, unit, err, &sg) || sg.start + blocks * kBlk >= sg.seq_len) return;
+    if (!this_segment(a, blocks, seg_div, unit, err, &sg) || sg.seq_len - sg.start <= blocks * kBlk) return;
 
     if (tid == 0) {
         for (int s = 0; s < kSegStages; ++s) {
@@ -255,6 +255,7 @@ linattn_segment_kernel(const __grid_constant__ LinattnMaps maps, const __grid_co
             }
         }
     }
+    settle(abort_flag);
     tc_fence_before();
     __syncthreads();
     if (warp == 1) {
@@ -720,6 +721,7 @@ linattn_output_kernel(const __grid_constant__ LinattnMaps maps, const __grid_con
         }
         if (leader) bulk_wait_group0();
     }
+    settle(abort_flag);
     tc_fence_before();
     __syncthreads();
     griddep_wait();

@@ -95,6 +95,12 @@ __device__ __forceinline__ bool mbar_wait_compact(uint64_t* bar, uint32_t parity
     return false;
 }
 
+// After a wait that expired: time for copies in flight to land before the CTA ends.
+__device__ __forceinline__ void settle(volatile int* abort) {
+    if (*abort)
+        for (int i = 0; i < 1000; ++i) __nanosleep(1000);
+}
+
 // ---------------------------------------------------------------- dependent launch
 // Lets the next kernel of the stream (launched with programmatic stream serialisation)
 // be scheduled once every CTA of this grid has executed this or exited.

@@ -52,6 +52,7 @@ def attn_step(lib, **kw):
 
 @pytest.mark.parametrize("kw,code", [
     (dict(dtype=2), DTYPE), (dict(total=-1), SHAPE), (dict(nseq=0), SHAPE), (dict(nseq=(1 << 20) + 1), SHAPE),
+    (dict(total=(1 << 31) - 1023), SHAPE),
     (dict(hq=0), SHAPE), (dict(hv=0), SHAPE), (dict(hv=5), SHAPE), (dict(hv=65536), SHAPE), (dict(dk=12), SHAPE),
     (dict(dv=0), SHAPE), (dict(dk=136, qs=272, ks=272), UNSUPPORTED), (dict(dv=256, vs=1024), UNSUPPORTED),
     (dict(qs=248), SHAPE), (dict(ks=260), SHAPE), (dict(vs=504), SHAPE), (dict(vs=1 << 40), SHAPE), (dict(q=0), NULL),
@@ -72,6 +73,7 @@ def test_linattn_step_refusals(lib, kw, code):
 
 @pytest.mark.parametrize("kw,code", [
     (dict(dtype=2), DTYPE), (dict(total=-1), SHAPE), (dict(nseq=0), SHAPE), (dict(hkv=0), SHAPE), (dict(hq=5), SHAPE),
+    (dict(total=(1 << 31) - 1023), SHAPE),
     (dict(dim=20), SHAPE), (dict(dim=136, qs=544, ks=272, vs=272), UNSUPPORTED), (dict(qs=504), SHAPE),
     (dict(ks=255), SHAPE), (dict(vs=8), SHAPE), (dict(q=0), NULL), (dict(cu=0), NULL), (dict(out=0), NULL),
     (dict(v=FAKE + 8), ALIGN), (dict(cu=FAKE + 1), ALIGN), (dict(total=0, q=0), OK)])
