@@ -7,6 +7,7 @@
 // running maximum m and sum of each row (one pass); exponentials are taken in base 2, with
 // log2(e) folded into the scale.
 #include "mixers.cuh"
+#include "prefill_tc.h"
 #include "ptx.cuh"
 
 namespace ssd {
@@ -52,6 +53,7 @@ attn_prefill_kernel(const AttnArgs a, const Divisor block, int* err)
     extern __shared__ float sm[];
     float *sq = sm, *sk = sq + kRows * kLd, *sv = sk + kKeys * kLd, *sp = sv + kKeys * kLd;
     const int h = blockIdx.y, tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    ptx::griddep_wait();                                   // every input may come from the kernel before
     if (blockIdx.x == 0 && h == 0) check_offsets(a.cu, a.nseq, a.total, err);
     int seq, j, first, len;
     // the blocks with the most keys first
@@ -192,8 +194,7 @@ cudaError_t prefill_d(const AttnArgs& a, cudaStream_t s)
     cudaError_t e = cudaFuncSetAttribute(attn_prefill_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)packed_blocks(a.total, a.nseq, kRows), (unsigned)a.hq);
-    attn_prefill_kernel<T, D><<<grid, kThreads, kBytes, s>>>(a, Divisor(kRows), device_error_word());
-    return cudaGetLastError();
+    return launch_dependent(attn_prefill_kernel<T, D>, grid, dim3(kThreads), kBytes, s, a, Divisor(kRows), device_error_word());
 }
 
 template <typename T>

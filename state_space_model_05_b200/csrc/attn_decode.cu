@@ -213,7 +213,8 @@ attn_decode_bf16_kernel(const __grid_constant__ CacheMaps maps, const AttnDecode
         *abort_flag = 0;
         fence_mbar_init();
     }
-    griddep_launch_dependents();
+    griddep_wait();                                        // every input may come from the kernel before
+    griddep_launch_dependents();                           // (only now: the join reads the lengths at once)
     const Units un(a.hq, a.hkv, kRows);
     const int c = blockIdx.x;
     const Located at = locate<kThreads>(a.lens, a.batch, a.capacity, un.per_row, false, c == 0 ? err : nullptr,
@@ -452,7 +453,8 @@ attn_decode_f32_kernel(const AttnDecodeArgs a, float* __restrict__ pieces, int* 
     extern __shared__ float smf[];
     float *sk = smf, *sv = sk + kTile * kLd, *sq = sv + kTile * kLd, *sp = sq + kRows32 * kMixMaxDim;
     __shared__ float sm_m[kRows32], sm_l[kRows32], sm_keep[kRows32];
-    griddep_launch_dependents();
+    griddep_wait();                                        // every input may come from the kernel before
+    griddep_launch_dependents();                           // (only now: the join reads the lengths at once)
     const int tid = threadIdx.x, c = blockIdx.x;
     const Units un(a.hq, a.hkv, kRows32);
     const Located at = locate<kThreads32>(a.lens, a.batch, a.capacity, un.per_row, false, c == 0 ? err : nullptr,
@@ -700,8 +702,7 @@ cudaError_t launch_bf16(const AttnDecodeArgs& a, float* pieces, cudaStream_t s)
     cudaError_t e = cudaFuncSetAttribute(attn_decode_bf16_kernel<D, kHigh>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kBytes);
     if (e != cudaSuccess) return e;
     const int G = decode_ctas(a.batch, a.capacity, a.hq, a.hkv, true);
-    attn_decode_bf16_kernel<D, kHigh><<<G, kThreads, Cfg<D>::kBytes, s>>>(maps, a, pieces, device_error_word());
-    e = cudaGetLastError();
+    e = launch_dependent(attn_decode_bf16_kernel<D, kHigh>, dim3(G), dim3(kThreads), Cfg<D>::kBytes, s, maps, a, pieces, device_error_word());
     return e != cudaSuccess ? e : launch_join<__nv_bfloat16, kRows>(a, pieces, G, s);
 }
 
@@ -724,8 +725,7 @@ cudaError_t launch_attn_decode(const AttnDecodeArgs& a, ssd_dtype_t dtype, void*
     cudaError_t e = cudaFuncSetAttribute(attn_decode_f32_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes32);
     if (e != cudaSuccess) return e;
     const int G = decode_ctas(a.batch, a.capacity, a.hq, a.hkv, false);
-    attn_decode_f32_kernel<<<G, kThreads32, kBytes32, s>>>(a, pieces, device_error_word());
-    e = cudaGetLastError();
+    e = launch_dependent(attn_decode_f32_kernel, dim3(G), dim3(kThreads32), kBytes32, s, a, pieces, device_error_word());
     return e != cudaSuccess ? e : launch_join<float, kRows32>(a, pieces, G, s);
 }
 

@@ -286,6 +286,8 @@ attn_prefill_tc_kernel(const __grid_constant__ AttnMaps maps, const __grid_const
         if (lane == 0) *abort_flag = 0;
         fence_mbar_init();
     }
+    // every input may come from the kernel before (and TMEM is not held while it may still need some)
+    griddep_wait();
     if (warp == kWarpMma) {
         tmem_alloc(tslot, 512);
         tmem_relinquish();
@@ -595,8 +597,8 @@ cudaError_t launch_t(const AttnArgs& a, cudaStream_t s)
     if (e != cudaSuccess) return e;
     const long long grid = (long long)packed_blocks(a.total, a.nseq, 2 * span) * a.hkv;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
-    attn_prefill_tc_kernel<D><<<(unsigned)grid, kThreads, Cfg<D>::kBytes, s>>>(maps, a, group, span, Divisor(2 * span), Divisor(a.hkv), device_error_word());
-    return cudaGetLastError();
+    return launch_dependent(attn_prefill_tc_kernel<D>, dim3((unsigned)grid), dim3(kThreads), Cfg<D>::kBytes, s, maps, a, group, span,
+                            Divisor(2 * span), Divisor(a.hkv), device_error_word());
 }
 
 }  // namespace

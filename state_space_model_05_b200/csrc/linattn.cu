@@ -121,14 +121,15 @@ __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
 template <typename T, int DK, int DV>
 __global__ void __launch_bounds__(kThreads)
-linattn_block_state_kernel(const LinattnArgs a, const Divisor block, float* __restrict__ states, int* err)
+linattn_block_state_kernel(const LinattnArgs a, const Divisor block, float* states, int* err)
 {
     constexpr int kLdK = DK + 4, kLdV = DV + 4, kR = DK / 16, kC = DV / 64;   // thread: kR rows, 4 kC columns
     extern __shared__ float sm[];
     __shared__ float sw[kTok];
     float *sk = sm, *sv = sm + kTok * kLdK;
     const int h = blockIdx.y, tid = threadIdx.x;
-    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();                                   // every input may come from the kernel before
+    ptx::griddep_launch_dependents();                      // (only now: the next kernels read inputs at once)
     if (blockIdx.x == 0 && h == 0) check_offsets(a.cu, a.nseq, a.total, err);
     int seq, j, first, len;
     if (!packed_block(a.cu, a.nseq, a.total, block, blockIdx.x, err, &seq, &j, &first, &len)) return;
@@ -372,8 +373,7 @@ cudaError_t prefill_d(const LinattnArgs& a, float* states, cudaStream_t s)
     if (e != cudaSuccess) return e;
     int* err = device_error_word();
     const dim3 grid((unsigned)packed_blocks(a.total, a.nseq, kTok), (unsigned)a.hv);
-    state_kernel<<<grid, kThreads, kStateBytes, s>>>(a, Divisor(kTok), states, err);
-    e = cudaGetLastError();
+    e = launch_dependent(state_kernel, grid, dim3(kThreads), kStateBytes, s, a, Divisor(kTok), states, err);
     const dim3 scan((unsigned)(a.nseq * a.hv), (unsigned)((a.dk * a.dv + 4 * kScanThreads - 1) / (4 * kScanThreads)));
     if (e == cudaSuccess) e = launch_dependent(linattn_scan_kernel, scan, dim3(kScanThreads), 0, s, a, states);
     if (e == cudaSuccess && a.total > 0)

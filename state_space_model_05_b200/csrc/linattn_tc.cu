@@ -152,6 +152,7 @@ linattn_segment_kernel(const __grid_constant__ LinattnMaps maps, const __grid_co
     Powers* pw = reinterpret_cast<Powers*>(sm + L::kPow);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int unit = hv_div.d > 1 ? hv_div.div(blockIdx.x) : (int)blockIdx.x, h = blockIdx.x - unit * a.hv;
+    griddep_wait();                                        // every input may come from the kernel before
     Segment sg;
     // the last segment of a sequence hands its state to no one
     if (!this_segment(a, blocks, seg_div, unit, err, &sg) || sg.seq_len - sg.start <= blocks * kBlk) return;
@@ -323,6 +324,9 @@ linattn_output_kernel(const __grid_constant__ LinattnMaps maps, const __grid_con
     Powers* pw = reinterpret_cast<Powers*>(sm + L::kPow);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int unit = hv_div.d > 1 ? hv_div.div(blockIdx.x) : (int)blockIdx.x, h = blockIdx.x - unit * a.hv;
+    // after a segment kernel, first segments start while its last ones run; without one, every input may
+    // come from the kernel before
+    if (a.total <= blocks * kBlk) griddep_wait();
     if (blockIdx.x == 0) check_offsets(a.cu, a.nseq, a.total, err);
     Segment sg;
     if (!this_segment(a, blocks, seg_div, unit, err, &sg)) {
@@ -815,15 +819,14 @@ cudaError_t launch_t(const LinattnArgs& a, float4* states, cudaStream_t s)
         e = cudaFuncSetAttribute(linattn_segment_kernel<DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  SegCfg<DK, DV>::kBytes);
         if (e != cudaSuccess) return e;
-        linattn_segment_kernel<DK, DV><<<(unsigned)grid, kSegThreads, SegCfg<DK, DV>::kBytes, s>>>(maps, a, blocks, seg_div, hv_div, states, err);
+        e = launch_dependent(linattn_segment_kernel<DK, DV>, dim3((unsigned)grid), dim3(kSegThreads), SegCfg<DK, DV>::kBytes, s, maps, a,
+                             blocks, seg_div, hv_div, states, err);
+        if (e != cudaSuccess) return e;
     }
     e = cudaFuncSetAttribute(linattn_output_kernel<DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, OutCfg<DK, DV>::kBytes);
     if (e != cudaSuccess) return e;
-    if (a.total > blocks * kBlk)                           // its first segments start while the segment kernel's last ones run
-        return launch_dependent(linattn_output_kernel<DK, DV>, dim3((unsigned)grid), dim3(kOutThreads), OutCfg<DK, DV>::kBytes, s, maps, a,
-                                blocks, seg_div, hv_div, states, err);
-    linattn_output_kernel<DK, DV><<<(unsigned)grid, kOutThreads, OutCfg<DK, DV>::kBytes, s>>>(maps, a, blocks, seg_div, hv_div, states, err);
-    return cudaGetLastError();
+    return launch_dependent(linattn_output_kernel<DK, DV>, dim3((unsigned)grid), dim3(kOutThreads), OutCfg<DK, DV>::kBytes, s, maps, a,
+                            blocks, seg_div, hv_div, states, err);
 }
 
 }  // namespace

@@ -169,3 +169,77 @@ def test_captured_steps_share_a_workspace(dtype):
         for z, old in zip(stack.tensors(), w[-1]):
             assert torch.equal(z.nan_to_num(7.0), old.nan_to_num(7.0))
     assert ssd.ssd_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", [bf, f32])
+@pytest.mark.parametrize("op", ["linattn_prefill", "linattn_step", "attn_prefill", "attn_step"])
+@pytest.mark.parametrize("eager", [True, False])
+def test_inputs_of_three_streams(dtype, op, eager):
+    """Queries written by a kernel of the call's own stream just before it, keys by a copy of a second
+    stream and values and lengths by kernels of a third: the call waits for all of them, eager and as a
+    node of a graph with several nodes before it; a replay sees new inputs."""
+    lens, n, dim, hq, hkv = [300, 0, 77, 1], 378, 64, 4, 2
+    rows = n if op.endswith("prefill") else len(lens)
+    src = [ref.randn(rows, h, dim, seed=60 + i, dtype=dtype) for i, h in enumerate((hq, hkv, hkv) if "attn_" in op and "lin" not in op else (hkv, hkv, hq))]
+    q, k, v = (torch.zeros_like(z) for z in src)
+    cu, given = ref.cu(lens), torch.tensor([9, 0, 63, 64], dtype=torch.int32, device="cuda")
+    ld, at = -0.1 * torch.ones(hq, device="cuda"), torch.zeros(4, dtype=torch.int32, device="cuda")
+    state = ref.randn(4, hq, dim, dim, seed=70)
+    kc, vc = (ref.randn(4, 80, hkv, dim, seed=71 + i, dtype=dtype) for i in range(2))
+    out = torch.empty(rows, hq, dim, dtype=dtype, device="cuda")
+    fin = torch.empty(4, hq, dim, dim, device="cuda")
+    ws = torch.empty(1 << 26, dtype=torch.uint8, device="cuda")
+    big = torch.ones(1 << 26, device="cuda")               # keeps each stream busy before it writes
+    streams = [torch.cuda.Stream() for _ in range(2)]
+
+    def run():
+        main = torch.cuda.current_stream()
+        for s in streams:
+            s.wait_stream(main)
+        with torch.cuda.stream(streams[0]):
+            big[:1 << 24].mul_(1.0)
+            k.copy_(src[1])
+        with torch.cuda.stream(streams[1]):
+            big[1 << 24:1 << 25].mul_(1.0)
+            torch.mul(src[2], 1, out=v)
+            torch.mul(given, 1, out=at)
+        big[1 << 25:].mul_(1.0)
+        torch.mul(src[0], 1, out=q)
+        for s in streams:
+            main.wait_stream(s)
+        if op == "linattn_prefill":
+            ssd.ssd_linattn_prefill(q, k, v, ld, cu, init_states=state, out=out, final_states=fin, workspace=ws)
+        elif op == "linattn_step":
+            ssd.ssd_linattn_decode_step(state, q, k, v, ld, out=out)
+        elif op == "attn_prefill":
+            ssd.ssd_attn_prefill(q, k, v, cu, out=out)
+        else:
+            ssd.ssd_attn_decode_step(kc, vc, at, q, k, v, out=out, workspace=ws)
+
+    def want():
+        if op == "linattn_prefill":
+            w = ref.linattn(*src, ld, lens, 1.0, state)
+            return w[0], w[2]
+        if op == "linattn_step":
+            w = ref.linattn_step(state, *src, ld, 1.0)
+            return w[0], w[2]
+        if op == "attn_prefill":
+            return ref.attn(*src, lens, dim ** -0.5)
+        return ref.attn_step(kc, vc, given.tolist(), *src, dim ** -0.5)
+
+    if not eager:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            run()
+    for i in range(3):
+        for z in (q, k, v, out):
+            z.zero_()
+        at.fill_(5)
+        src[0].mul_(-1)
+        src[2].mul_(-0.5)
+        expected, tol = want()
+        torch.cuda.synchronize()
+        run() if eager else graph.replay()
+        torch.cuda.synchronize()
+        ref.assert_within(out, expected, tol, f"{op}, run {i}")
+    assert ssd.ssd_device_status() == 0
