@@ -294,7 +294,8 @@ ssd_status_t ssd_gdn_decode_step(float* state, const void* q, const void* k, con
  *   log_decay [heads_v] fp32: <= 0 for a contracting state (any value but NaN and +inf is
  *          computed as given; -inf keeps only the token itself)
  *   init_states / final_states [nseq][heads_v][dk][dv] fp32; NULL init_states means zeros;
- *          the two may be the same buffer.  An empty sequence's final state is its initial one.
+ *          the two may be the same buffer, but not overlap in part.  An empty sequence's final
+ *          state is its initial one.
  *   cu_seqlens: DEVICE array of nseq + 1 int32 offsets, cu_seqlens[0] = 0, non-decreasing, the
  *          last at most total_tokens.  Rows of `out` behind the last sequence are left as they
  *          were.  Offsets that break this record SSD_ERR_SHAPE in the device error word; the

@@ -160,8 +160,18 @@ linattn_segment_kernel(const __grid_constant__ LinattnMaps maps, const __grid_co
     const int unit = hv_div.d > 1 ? hv_div.div(blockIdx.x) : (int)blockIdx.x, h = blockIdx.x - unit * a.hv;
     griddep_wait();                                        // every input may come from the kernel before
     Segment sg;
-    // the last segment of a sequence hands its state to no one
-    if (!this_segment(a, blocks, seg_div, unit, err, &sg) || sg.seq_len - sg.start <= blocks * kBlk) return;
+    if (!this_segment(a, blocks, seg_div, unit, err, &sg)) return;
+    if (sg.seq_len - sg.start <= blocks * kBlk) {
+        // the last segment of a sequence hands its state to no one; where the final states replace the
+        // initial ones, it keeps the sequence's for the segments, some of which may start after
+        // another has written the final state
+        if (sg.j > 0 && a.init_states == a.final_states) {
+            const size_t elems = (size_t)a.dk * a.dv;
+            const float4* src = reinterpret_cast<const float4*>(a.init_states + ((size_t)sg.seq * a.hv + h) * elems);
+            for (int i = threadIdx.x; i < (int)(elems / 4); i += kSegThreads) states[(size_t)blockIdx.x * (DK * DV / 4) + i] = src[i];
+        }
+        return;
+    }
 
     if (tid == 0) {
         for (int s = 0; s < kSegStages; ++s) {
@@ -550,10 +560,16 @@ linattn_output_kernel(const __grid_constant__ LinattnMaps maps, const __grid_con
         const bool mine = row < a.dk;
         float S[NC];
         const size_t at = (((size_t)sg.seq * a.hv + h) * a.dk + row) * a.dv + c0;
+        const float* init = a.init_states ? a.init_states + at : nullptr;
+        if (init && a.init_states == a.final_states && sg.seq_len > blocks * kBlk) {
+            griddep_wait();                                // kept in the last segment's place (linattn_segment_kernel)
+            const size_t place = blockIdx.x + (size_t)((sg.seq_len - 1) / (blocks * kBlk) - sg.j) * a.hv;
+            init = reinterpret_cast<const float*>(states + place * (DK * DV / 4)) + (size_t)row * a.dv + c0;
+        }
 #pragma unroll
         for (int e = 0; e < NC; e += 4) {
             float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (a.init_states && mine && c0 + e < a.dv) x = *reinterpret_cast<const float4*>(a.init_states + at + e);
+            if (init && mine && c0 + e < a.dv) x = *reinterpret_cast<const float4*>(init + e);
             S[e] = x.x; S[e + 1] = x.y; S[e + 2] = x.z; S[e + 3] = x.w;
         }
         if (sg.j > 0) {

@@ -142,6 +142,21 @@ def test_state_buffer_may_be_reused():
     assert fin2 is buf and torch.equal(out, out2) and torch.equal(fin, fin2)
 
 
+@pytest.mark.parametrize("dtype", [bf, f32])
+@pytest.mark.parametrize("hv,dk,dv", [(8, 128, 128), (6, 40, 72), (40, 128, 64)])
+def test_state_buffer_may_be_reused_by_long_prompts(dtype, hv, dk, dv):
+    """Sequences whose parts run side by side, each of which starts from the initial state that the
+    last one replaces; decays near 1, so that it counts to the end."""
+    lens = [2500, 1, 0, 3001, 130]
+    q, k, v, ld, s0 = problem(lens, 2, hv, dk, dv, dtype, seed=15, init=True)
+    ld, s0 = ld * 1e-4, s0 * 30
+    out, fin = check(lens, q, k, v, ld, s0, 0.1, "separate states")
+    for _ in range(3):
+        buf = s0.clone()
+        out2, fin2 = ssd.ssd_linattn_prefill(q, k, v, ld, ref.cu(lens), scale=0.1, init_states=buf, final_states=buf)
+        assert fin2 is buf and torch.equal(out, out2) and torch.equal(fin, fin2)
+
+
 def test_no_tokens_copies_the_states():
     z = lambda *s: torch.zeros(s, device="cuda", dtype=bf)
     s0 = ref.randn(2, 2, 64, 64, seed=13)
