@@ -243,3 +243,36 @@ def test_inputs_of_three_streams(dtype, op, eager):
         torch.cuda.synchronize()
         ref.assert_within(out, expected, tol, f"{op}, run {i}")
     assert ssd.ssd_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", [bf, f32])
+def test_calls_at_once_on_several_streams(dtype):
+    """Calls of three kinds on streams of their own, again and again: bit for bit what each gives alone."""
+    lens = [700, 0, 33, 1500, 129]
+    n, dim = sum(lens), 64
+    q, k, v = (ref.randn(n, h, dim, seed=80 + i, dtype=dtype) for i, h in enumerate((8, 4, 4)))
+    cu, ld, s0 = ref.cu(lens), -0.01 * torch.ones(8, device="cuda"), ref.randn(5, 8, dim, dim, seed=84)
+    kc, vc = (ref.randn(5, 900, 4, dim, seed=85 + i, dtype=dtype) for i in range(2))
+    at = torch.tensor([899, 0, 400, 64, 3], dtype=torch.int32, device="cuda")
+    wide = ref.randn(n, 8, dim, seed=87, dtype=dtype)
+    calls = [lambda: ssd.ssd_linattn_prefill(k, v, wide, ld, cu, init_states=s0),
+             lambda: (ssd.ssd_attn_prefill(q, k, v, cu),),
+             lambda: (ssd.ssd_attn_decode_step(kc, vc, at, q[:5], k[:5], v[:5]),),
+             lambda: ssd.ssd_linattn_prefill(k, wide[:, :4].contiguous(), wide, ld, cu)]
+    want = []
+    for call in calls:
+        want.append(call())
+        torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    got = [[] for _ in calls]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(8):
+        for i, (call, s) in enumerate(zip(calls, streams)):
+            with torch.cuda.stream(s):
+                got[i].append(call())
+    torch.cuda.synchronize()
+    for i, w in enumerate(want):
+        for g in got[i]:
+            assert all(torch.equal(x, y) for x, y in zip(g, w)), i
+    assert ssd.ssd_device_status() == 0
