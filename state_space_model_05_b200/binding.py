@@ -423,14 +423,14 @@ def ssd_linattn_prefill(q, k, v, log_decay, cu_seqlens, scale=1.0, init_states=N
                  ((log_decay, "log_decay", (hv,), f32), (cu_seqlens, "cu_seqlens", (nseq + 1,), torch.int32),
                   (init_states, "init_states", state_shape, f32), (out, "out", out_shape, dtype),
                   (final_states, "final_states", state_shape, f32), (workspace, "workspace", None, None)))
-    code, device = _dtype_code(q), q.device
+    code = _dtype_code(q)
     if out is None:
-        out = torch.empty(out_shape, dtype=dtype, device=device)
+        out = q.new_empty(out_shape)
     if final_states is None:
-        final_states = torch.empty(state_shape, dtype=f32, device=device)
+        final_states = log_decay.new_empty(state_shape)
     if workspace is None:
-        workspace = torch.empty(_workspace_bytes("ssd_linattn_prefill_workspace_bytes", nseq, total, hq, hv, dk, dv, code),
-                                dtype=torch.uint8, device=device)
+        workspace = q.new_empty(_workspace_bytes("ssd_linattn_prefill_workspace_bytes", nseq, total, hq, hv, dk, dv, code),
+                                dtype=torch.uint8)
     st = lib().ssd_linattn_prefill(_ptr(q), _ptr(k), _ptr(v), _packed(q), _packed(k), _packed(v), _ptr(log_decay),
                                    _ptr(init_states), _ptr(cu_seqlens), nseq, total, hq, hv, dk, dv, scale, code,
                                    _ptr(out), _ptr(final_states), _ptr(workspace), _nbytes(workspace), _stream(stream))
@@ -473,7 +473,7 @@ def ssd_attn_prefill(q, k, v, cu_seqlens, scale=None, out=None, stream=None):
                  ((cu_seqlens, "cu_seqlens", (nseq + 1,), torch.int32), (out, "out", out_shape, q.dtype)))
     code = _dtype_code(q)
     if out is None:
-        out = torch.empty(out_shape, dtype=q.dtype, device=q.device)
+        out = q.new_empty(out_shape)
     st = lib().ssd_attn_prefill(_ptr(q), _ptr(k), _ptr(v), _packed(q), _packed(k), _packed(v), _ptr(cu_seqlens),
                                 nseq, total, hq, hkv, dim, dim ** -0.5 if scale is None else scale,
                                 code, _ptr(out), _stream(stream))
@@ -500,8 +500,8 @@ def ssd_attn_decode_step(k_cache, v_cache, cache_lens, q, k, v, scale=None, out=
     if out is None:
         out = torch.empty_like(q)
     if workspace is None:
-        workspace = torch.empty(_workspace_bytes("ssd_attn_decode_workspace_bytes", batch, capacity, hq, hkv, dim, code),
-                                dtype=torch.uint8, device=q.device)
+        workspace = q.new_empty(_workspace_bytes("ssd_attn_decode_workspace_bytes", batch, capacity, hq, hkv, dim, code),
+                                dtype=torch.uint8)
     st = lib().ssd_attn_decode_step(_ptr(k_cache), _ptr(v_cache), _ptr(cache_lens), _ptr(q), _ptr(k), _ptr(v), batch,
                                     capacity, hq, hkv, dim, dim ** -0.5 if scale is None else scale, code, _ptr(out),
                                     _ptr(workspace), _nbytes(workspace), _stream(stream))
