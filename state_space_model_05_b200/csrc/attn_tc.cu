@@ -20,12 +20,13 @@
 // announces S_i also covers P V_(i-1), issued before it.  P is rounded to bf16 (the operand type; its sum is
 // taken before the rounding, in fp32), as is the output; everything else is fp32.
 //
-// Bound by the products and the exponentials together: per 128 x 128 scores the products took 770 clocks at 64
-// dimensions and 1460 at 128 when timed alone, and 16384 exponentials take 1024 at 16 a clock.  Measured, 16384 tokens, 16/4 heads of 128: 837 us = 1.31 PFLOP/s at 1.9 GHz, 1.0 ms = 1.10 PFLOP/s
-// under the power limit (a large library matrix product: 1.67 and 1.43).  32 x 512 tokens,
+// Bound by the products and the exponentials together: per 128 x 128 scores the products took 770
+// clocks at 64 dimensions and 1460 at 128 when timed alone, and 16384 exponentials take 1024 at 16 a
+// clock.  Measured, 16384 tokens, 16/4 heads of 128: 832 us = 1.32 PFLOP/s at 1.9 GHz, 1.0 ms =
+// 1.10 PFLOP/s under the power limit (a large library matrix product: 1.67 and 1.43).  32 x 512 tokens,
 // 32/8 heads of 64: 93 us, 116 us at the clocks where one block per CTA took 164.  Without turns at the
-// exponentials: 903 us instead of 832, 98 instead of 93.  Heads of up to 64 dimensions have tiles
-// of 64, which leaves room for twice the slots: 8192 tokens, 32/8 heads of 64: 370 us, 413 us on the tiles of 128.
+// exponentials: 903 us instead of 832, 98 instead of 93.  Heads of up to 64 dimensions have tiles of 64,
+// which leaves room for twice the slots: 8192 tokens, 32/8 heads: 370 us, 413 us on the tiles of 128.
 #include <cuda.h>
 
 #include "mixers.cuh"
