@@ -276,3 +276,22 @@ def test_calls_at_once_on_several_streams(dtype):
         for g in got[i]:
             assert all(torch.equal(x, y) for x, y in zip(g, w)), i
     assert ssd.ssd_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", [bf, f32])
+def test_most_sequences_and_most_heads(dtype):
+    """2^20 sequences of one token, and 65535 heads: a lone token's attention is its own value, and its
+    linear attention's state k v^T."""
+    for n, heads, offsets in ((1 << 20, 1, None), (2, 65535, [0, 1, 2])):
+        cu = torch.arange(n + 1, dtype=torch.int32, device="cuda") if offsets is None else ref.cu([1, 1])
+        q, k, v = (ref.randn(n, heads, 8, seed=90 + i, dtype=dtype) for i in range(3))
+        assert torch.equal(ssd.ssd_attn_prefill(q, k, v, cu), v)
+        out, fin = ssd.ssd_linattn_prefill(q, k, v, torch.zeros(heads, device="cuda"), cu)
+        kv = k.double()[..., :, None] * v.double()[..., None, :]
+        # one rounding of a product, or its value as a sum of three bf16 numbers
+        assert ((fin.double() - kv).abs() <= 2.0 ** -23 * kv.abs()).all()
+        want = (q.double() * k.double()).sum(-1, keepdim=True) * v.double()
+        size = (q.double() * k.double()).abs().sum(-1, keepdim=True) * v.double().abs()
+        half = ref.HALF[dtype]                             # of the score and of the output, and fp32 sums
+        assert ((out.double() - want).abs() <= half * want.abs() + ((half if dtype == bf else 0.0) + 12 * ref.F32) * size * (1 + half)).all()
+    assert ssd.ssd_device_status() == 0
