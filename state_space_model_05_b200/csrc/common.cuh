@@ -59,6 +59,10 @@ struct Dims {
     const int* vl_seq = nullptr;      // device [nchunks] sequence of each block, -1 past the total
 };
 
+// Whether a and b, a packed sequence's offset and the next one's, bound a range of the tokens.  Any
+// 32-bit values may be asked about: the offsets are compared as they are, since b - a may overflow.
+__host__ __device__ inline bool valid_offsets(int a, int b, int total) { return a >= 0 && a <= b && b <= total; }
+
 // Rows of block kb in packed variable-length mode: false if kb holds no tokens.
 __device__ __forceinline__ bool varlen_block(const int* cu, const int* first, const int* seqof, int kb,
                                              int Q, int* seq, int* t0, int* len) {

@@ -191,12 +191,13 @@ linattn_scan_kernel(const LinattnArgs a, float* states)
     const int seq = blockIdx.x / a.hv, h = blockIdx.x - seq * a.hv;
     const int e = (blockIdx.y * kScanThreads + threadIdx.x) * 4, elems = a.dk * a.dv;
     ptx::griddep_launch_dependents();
-    const int first = a.cu[seq], len = a.cu[seq + 1] - first;
+    const int first = a.cu[seq], end = a.cu[seq + 1];
     const float ld = a.log_decay[h];
     const size_t base = (size_t)blockIdx.x * elems + e;
     float4 H = a.init_states && e < elems ? *reinterpret_cast<const float4*>(a.init_states + base) : make_float4(0.f, 0.f, 0.f, 0.f);
     ptx::griddep_wait();
-    if (e >= elems || first < 0 || len < 0 || first + len > a.total) return;      // (offsets reported by the blocks)
+    if (e >= elems || !valid_offsets(first, end, a.total)) return;      // (offsets reported by the blocks)
+    const int len = end - first;
     float* U = states + ((size_t)(first / kTok + seq) * a.hv + h) * elems + e;
     const size_t step = (size_t)a.hv * elems;
     const int blocks = (len + kTok - 1) / kTok;

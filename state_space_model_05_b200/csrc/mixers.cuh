@@ -75,7 +75,7 @@ __device__ __forceinline__ bool packed_block(const int* __restrict__ cu, int nse
         n = min(step, n - k * step);
     }
     const int a = cu[lo], b = cu[lo + 1];
-    if (a < 0 || b < a || b > total) {
+    if (!valid_offsets(a, b, total)) {
         record_error(err, SSD_ERR_SHAPE);
         return false;
     }
@@ -92,7 +92,7 @@ __device__ __forceinline__ void check_offsets(const int* __restrict__ cu, int ns
 {
     bool bad = false;
     for (int s = threadIdx.x; s < nseq; s += blockDim.x)
-        bad |= cu[s + 1] < cu[s] || cu[s + 1] > total || (s == 0 && cu[0] != 0);
+        bad |= !valid_offsets(cu[s], cu[s + 1], total) || (s == 0 && cu[0] != 0);
     if (bad) record_error(err, SSD_ERR_SHAPE);
 }
 

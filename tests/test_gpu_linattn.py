@@ -243,3 +243,18 @@ def test_prefill_then_steps_is_prefill(dtype):
     wo, wf, to, tf = ref.linattn(q, k, v, ld, [205], 0.1, s0)
     ref.assert_within(torch.cat([out, *outs]), wo, to, "outputs")
     ref.assert_within(state, wf, tf, "state")
+
+
+@pytest.mark.parametrize("dtype", [bf, f32])
+def test_offsets_whose_difference_overflows_touch_nothing(dtype):
+    """A next offset near the lowest 32-bit value: reported, and neither the workspace's surroundings
+    nor the states of that sequence are written."""
+    q, k, v, ld, _ = problem([100], 1, 2, 64, 64, dtype, seed=18)
+    cu = torch.tensor([0, 100, -(1 << 31) + 50, 100], dtype=torch.int32, device="cuda")
+    need = ssd.binding.lib().ssd_linattn_prefill_workspace_bytes(3, 100, 1, 2, 64, 64, 0 if dtype == f32 else 1)
+    room = torch.full((need + (64 << 20),), 77, dtype=torch.uint8, device="cuda")
+    fin = torch.full((3, 2, 64, 64), 7.0, device="cuda")
+    ssd.ssd_linattn_prefill(q, k, v, ld, cu, final_states=fin, workspace=room[32 << 20:(32 << 20) + need])
+    assert ssd.ssd_device_status() == 2                      # SSD_ERR_SHAPE
+    assert bool((room[:32 << 20] == 77).all()) and bool((room[(32 << 20) + need:] == 77).all())
+    assert bool((fin[1:] == 7.0).all())
