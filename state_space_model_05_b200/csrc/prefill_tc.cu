@@ -71,13 +71,17 @@ varlen_table_kernel(const int* __restrict__ cu, int nseq, int total_tokens, int 
     __syncthreads();
     const int per = (nseq + kTableThreads - 1) / kTableThreads;
     const int s0 = min(nseq, tid * per), s1 = min(nseq, s0 + per);
-    int sum = 0, neg = 0;
+    // valid offsets' blocks number at most total_tokens / Q + nseq; others are not counted
+    auto blocks_of = [&](int s) { return cu[s + 1] > cu[s] ? (cu[s + 1] - cu[s] - 1) / Q + 1 : 0; };
+    int sum = 0;
+    bool wrong = false;
     for (int s = s0; s < s1; ++s) {
-        const int len = cu[s + 1] - cu[s];
-        neg |= len < 0;
-        sum += (max(len, 0) + Q - 1) / Q;
+        if (valid_offsets(cu[s], cu[s + 1], total_tokens))
+            sum += blocks_of(s);
+        else
+            wrong = true;
     }
-    if (neg) atomicOr(&bad, 1);
+    if (wrong) atomicOr(&bad, 1);
     part[tid] = sum;
     __syncthreads();
     for (int o = 1; o < kTableThreads; o <<= 1) {      // inclusive scan of the partial counts
@@ -96,7 +100,7 @@ varlen_table_kernel(const int* __restrict__ cu, int nseq, int total_tokens, int 
     int base = tid ? part[tid - 1] : 0;
     for (int s = s0; s < s1; ++s) {
         first[s] = base;
-        const int nb = (cu[s + 1] - cu[s] + Q - 1) / Q;
+        const int nb = blocks_of(s);
         for (int k = 0; k < nb; ++k) seqof[base + k] = s;
         base += nb;
     }

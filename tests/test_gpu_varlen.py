@@ -162,3 +162,24 @@ def test_cuda_core_equal_lengths_equal_batched_call_bitwise():
                                     C.reshape(600, 1, 64), D, cu, 64)
     torch.cuda.synchronize()
     assert torch.equal(y1.reshape(600, 4, 32), y2) and torch.equal(s1, s2)
+
+
+@pytest.mark.parametrize("bf16,Q", [(True, 256), (False, 64)])
+@pytest.mark.parametrize("bad", [[0, 1000, -(1 << 31) + 999, 400], [0, 100, -(1 << 31) + 50, 400], [0, -5, 200, 400], [0, 401, 401, 400]])
+def test_bad_offsets_at_the_ends_of_32_bits(bf16, Q, bad):
+    """Offsets whose differences overflow, or that lie outside the tokens: reported, nothing computed,
+    and the workspace's surroundings are left as they were."""
+    import state_space_model_05_b200 as ssd
+    inp, _, T = _packed([200, 200], seed=6)
+    dt_ = torch.bfloat16 if bf16 else torch.float32
+    lib = ssd.binding.lib()
+    need = lib.ssd_prefill_varlen_workspace_bytes(3, T, 4, 64, 1, 128, Q, 1 if bf16 else 0)
+    room = torch.full((need + (128 << 20),), 77, dtype=torch.uint8, device="cuda")
+    y = torch.zeros((T, 4, 64), device="cuda", dtype=dt_)
+    ssd.ssd_prefill_varlen(to_dev(inp.x[0, :T], dt_), to_dev(inp.dt[0, :T], torch.float32), to_dev(inp.A, torch.float32),
+                           to_dev(inp.B[0, :T], dt_), to_dev(inp.C[0, :T], dt_), to_dev(inp.D, torch.float32),
+                           torch.tensor(bad, dtype=torch.int32, device="cuda"), Q, y=y, workspace=room[64 << 20:(64 << 20) + need])
+    torch.cuda.synchronize()
+    assert ssd.ssd_device_status() == 2               # SSD_ERR_SHAPE
+    assert torch.count_nonzero(y) == 0
+    assert bool((room[:64 << 20] == 77).all()) and bool((room[(64 << 20) + need:] == 77).all())

@@ -59,3 +59,13 @@ def test_a_length_formed_first_would_not_do(check):
              if length_first(a, b, TOTAL) and not 0 <= a <= b <= TOTAL]
     assert (100, LOW + 50, TOTAL) in cases and all(a > TOTAL or wrap(b - a) > TOTAL for a, b, _ in cases)
     assert not any(check(cases))
+
+
+def test_a_table_of_wrapped_lengths_would_not_do(check):
+    """Offsets of three sequences whose wrapped lengths are all positive and whose wrapped block counts
+    sum to what the table has room for: the last sequence's blocks would lie far before the table."""
+    cu, block = [0, 1000, LOW + 999, TOTAL], 128
+    lens = [wrap(b - a) for a, b in zip(cu, cu[1:])]
+    blocks = [int(wrap(n + block - 1) / block) for n in lens]
+    assert min(lens) >= 0 and sum(blocks) <= TOTAL // block + len(lens) and sum(blocks[:2]) < -(1 << 23)
+    assert check([(a, b, TOTAL) for a, b in zip(cu, cu[1:])]) == [False, False, False]
