@@ -673,7 +673,7 @@ attn_decode_join_kernel(const AttnDecodeArgs a, const float* pieces, int max_cta
 int decode_ctas(int batch, int capacity, int hq, int hkv, bool bf16)
 {
     const Units un(hq, hkv, bf16 ? kRows : kRows32);
-    const long long tiles = (long long)batch * un.per_row * ((capacity + kTile - 1) / kTile);
+    const long long tiles = (long long)batch * un.per_row * ((capacity - 1) / kTile + 1);
     const long long fit = (long long)tc_sm_count() * (bf16 ? 2 : 3);
     return (int)(tiles < fit ? tiles : fit);
 }

@@ -199,3 +199,12 @@ def test_reference_forms_agree():
         o, state, _, _ = ref.linattn_step(state, q[t:t + 1], k[t:t + 1], v[t:t + 1], ld, 0.5)
         torch.testing.assert_close(o[0], out[t], rtol=1e-10, atol=1e-10)
     torch.testing.assert_close(state, final, rtol=1e-10, atol=1e-10)
+
+
+@pytest.mark.parametrize("dtype", [0, 1])
+@pytest.mark.parametrize("capacity", [(1 << 31) - 1, (1 << 31) - 64, (1 << 31) - 65])
+def test_workspace_of_the_largest_caches(lib, capacity, dtype):
+    """A cache of any capacity needs no more pieces than CTAs fit the GPU at once."""
+    aw = lib.ssd_attn_decode_workspace_bytes
+    assert aw(1, capacity, 4, 2, 128, dtype) == aw(1, 1 << 20, 4, 2, 128, dtype)
+    assert attn_step(lib, capacity=capacity, nbytes=aw(3, capacity, 4, 2, 128, dtype) - 1, dtype=dtype) == WORKSPACE
