@@ -296,29 +296,104 @@ struct OutCfg {
     static constexpr int kPow = kConv + kConvSlots * kSlot;
     static constexpr int kBar = (kPow + (int)sizeof(Powers) + 7) / 8 * 8;
     static constexpr int kTm = kBar + 32 * 8;
-    static constexpr int kBytes = kTm + 32 + 1024;
+    static constexpr int kBytes = kTm + 64 + 1024;
     static_assert(kBytes <= 227 * 1024, "shared memory");
     // TMEM columns: scores (then P), the block's part, the carried part, the block's state
     static constexpr uint32_t kS = 0, kYd = 128, kYo = 256, kU = 384;
 };
 
-// One output of a row from the row's own sum over its block, which holds a value that is not
-// finite: only the rows from that token on see it (the product's zeros would not hide it).
-__device__ __noinline__ float own_sum(const LinattnArgs& a, const Powers* pw, size_t base, int r, int h, int col)
+__device__ __forceinline__ bool not_finite(uint32_t bf16_bits) { return (bf16_bits & 0x7F80u) == 0x7F80u; }
+
+// Takes the values that are not finite out of a thread's chunks of a block's tile and marks their tokens
+// (a bit each): P's zeros would not hide them from the rows before them.
+template <int DV>
+__device__ __forceinline__ void take_out_bad_values(uint8_t* values, int odd, int gt, unsigned* tokens)
 {
+#pragma unroll 1
+    for (int p = odd; p < kPieces<DV>; p += 2) {
+        int t;
+        uint4* at = piece_chunk<DV>(values, p, gt, &t);
+        const uint4 u = *at;
+        uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        bool any = false;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const bool lo = not_finite(w[j]), hi = not_finite(w[j] >> 16);
+            any |= lo || hi;
+            w[j] &= (lo ? 0u : 0xFFFFu) | (hi ? 0u : 0xFFFF0000u);
+        }
+        if (any) {
+            *at = make_uint4(w[0], w[1], w[2], w[3]);
+            atomicOr(&tokens[t >> 5], 1u << (t & 31));
+        }
+    }
+}
+
+// Adds those values, times their scores, to the staged outputs of row r (`row`, its 16-byte chunks
+// permuted by the row): g^(r-s) (q_r.k_s) v_s from the tokens s <= r marked in `tokens`.  Only the sign
+// of a score matters, or that it is zero.  Rare, and called by whole warps.
+template <int DV>
+__device__ __noinline__ void add_bad_values(const LinattnArgs& a, const Powers* pw, uint8_t* row, const unsigned* tokens, size_t base,
+                                            int r, int rows, int h)
+{
+    auto chunk = [&](int ch) { return reinterpret_cast<uint4*>(row + (ch >> 3) * kHalf + (((ch & 7) ^ (r & 7)) << 4)); };
+    // where every output is NaN already (a state that holds NaN), there is nothing to add
+    bool all = true;
+#pragma unroll 1
+    for (int ch = 0; 8 * ch < a.dv && r < rows; ++ch) {
+        const uint4 u = *chunk(ch);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) all = all && (w[j] & 0x7FFFu) > 0x7F80u && (w[j] >> 16 & 0x7FFFu) > 0x7F80u;
+    }
+    if (__all_sync(0xffffffffu, all)) return;
     const size_t hq = (size_t)(h / (a.hv / a.hq)) * a.dk;
     const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + (base + r) * a.q_stride + hq;
-    float y = 0.f;
 #pragma unroll 1
-    for (int s = 0; s <= r; ++s) {
-        const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(a.k) + (base + s) * a.k_stride + hq;
-        float p = 0.f;
+    for (int i = 0; i < 4; ++i) {
 #pragma unroll 1
-        for (int d = 0; d < a.dk; ++d) p = fmaf(__bfloat162float(q[d]), __bfloat162float(k[d]), p);
-        y = fmaf(p * pw->up[r - s],
-                 __bfloat162float(static_cast<const __nv_bfloat16*>(a.v)[(base + s) * a.v_stride + (size_t)h * a.dv + col]), y);
+        for (unsigned left = tokens[i]; left; left &= left - 1) {
+            const int s = 32 * i + __ffs(left) - 1;
+            if (s > r || r >= rows) continue;
+            const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(a.k) + (base + s) * a.k_stride + hq;
+            const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.v) + (base + s) * a.v_stride + (size_t)h * a.dv;
+            float score = 0.f;                             // formed where an infinity needs it
+            bool formed = false;
+#pragma unroll 1
+            for (int ch = 0; 8 * ch < a.dv; ++ch) {
+                const uint4 vv = *reinterpret_cast<const uint4*>(v + 8 * ch);
+                const uint32_t x[4] = {vv.x, vv.y, vv.z, vv.w};
+                bool any = false, inf = false;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    any |= not_finite(x[j]) || not_finite(x[j] >> 16);
+                    inf |= (x[j] & 0x7FFFu) == 0x7F80u || (x[j] >> 16 & 0x7FFFu) == 0x7F80u;
+                }
+                if (!any) continue;
+                if (inf && !formed) {
+#pragma unroll 1
+                    for (int d = 0; d < a.dk; d += 8) {
+                        const uint4 qq = *reinterpret_cast<const uint4*>(q + d), kk = *reinterpret_cast<const uint4*>(k + d);
+                        const uint32_t y[4] = {qq.x, qq.y, qq.z, qq.w}, z[4] = {kk.x, kk.y, kk.z, kk.w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) score = fmaf(bf16hi(y[j]), bf16hi(z[j]), fmaf(bf16lo(y[j]), bf16lo(z[j]), score));
+                    }
+                    score *= pw->up[r - s];
+                    formed = true;
+                }
+                uint4* at = chunk(ch);
+                const uint4 u = *at;
+                uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float lo = not_finite(x[j]) ? score * bf16lo(x[j]) * a.scale : 0.f;
+                    const float hi = not_finite(x[j] >> 16) ? score * bf16hi(x[j]) * a.scale : 0.f;
+                    w[j] = pack_bf16x2(bf16lo(w[j]) + lo, bf16hi(w[j]) + hi);
+                }
+                *at = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        }
     }
-    return y;
 }
 
 template <int DK, int DV>
@@ -337,6 +412,7 @@ linattn_output_kernel(const __grid_constant__ LinattnMaps maps, const __grid_con
     uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + L::kTm);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L::kTm + 4);
     volatile int* bad_values = reinterpret_cast<volatile int*>(sm + L::kTm + 8);     // [4], by block mod 4
+    unsigned* bad_tokens = reinterpret_cast<unsigned*>(sm + L::kTm + 24);            // [2][4], by block mod 2
     Powers* pw = reinterpret_cast<Powers*>(sm + L::kPow);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int unit = hv_div.d > 1 ? hv_div.div(blockIdx.x) : (int)blockIdx.x, h = blockIdx.x - unit * a.hv;
@@ -379,6 +455,7 @@ linattn_output_kernel(const __grid_constant__ LinattnMaps maps, const __grid_con
         }
         *abort_flag = 0;
         for (int i = 0; i < 4; ++i) bad_values[i] = 0;
+        for (int i = 0; i < 8; ++i) bad_tokens[i] = 0u;
         fence_mbar_init();
     }
     const float ld = a.log_decay[h];
@@ -400,8 +477,8 @@ linattn_output_kernel(const __grid_constant__ LinattnMaps maps, const __grid_con
     constexpr int QS = L::kQSlots;
     // The pieces of block c's V~ whose number is `odd` mod 2, formed by 256 threads.  On the way the
     // values themselves are looked after: rows behind the sequence's end are another's and zeroed,
-    // since 0 x inf is not 0; values that are not finite are left to the output warps, as P's zeros
-    // would not hide them.
+    // since 0 x inf is not 0; values that are not finite are taken out and left to the output warps, as
+    // P's zeros would not hide them.
     auto weighted_values = [&](int c, int odd, int gt) {
         const int rows = tokens(c);
         if (!wait_warp(&v_full[c & 1], c / 2)) return false;
@@ -438,7 +515,10 @@ linattn_output_kernel(const __grid_constant__ LinattnMaps maps, const __grid_con
             if (lane == 0) mbar_arrive(&conv_full[odd]);
         }
         const __nv_bfloat162 all = __hadd2(__hadd2(acc[0], acc[1]), __hadd2(acc[2], acc[3]));
-        if (__hisnan(all.x) || __hisnan(all.y)) bad_values[c & 3] = c + 1;
+        if (__hisnan(all.x) || __hisnan(all.y)) {
+            bad_values[c & 3] = c + 1;
+            take_out_bad_values<DV>(vslot(c), odd, gt, bad_tokens + 4 * (c & 1));
+        }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&v_ok[c & 1]);
@@ -709,24 +789,15 @@ linattn_output_kernel(const __grid_constant__ LinattnMaps maps, const __grid_con
                     *reinterpret_cast<uint4*>(stage + (q >> 1) * kHalf + ((((q & 1) * 4 + e / 8) ^ (r & 7)) << 4)) =
                         make_uint4(o[0], o[1], o[2], o[3]);
                 }
-                if (bad) {
-                    // (rare: the staged row again, a column at a time)
-#pragma unroll 1
-                    for (int e = 0; e < 32; ++e) {
-                        uint32_t carried;
-                        tmem_ld1(tmem + lanes + L::kYo + 32 * q + e, carried);
-                        tmem_wait_ld();
-                        if (r < rows && 32 * q + e < a.dv)
-                            *reinterpret_cast<__nv_bfloat16*>(stage + (q >> 1) * kHalf + ((((q & 1) * 4 + (e >> 3)) ^ (r & 7)) << 4) + 2 * (e & 7)) =
-                                __float2bfloat16_rn(a.scale * fmaf(g_out, __uint_as_float(carried), own_sum(a, pw, base, r, h, 32 * q + e)));
-                    }
-                }
             }
+            if (bad) add_bad_values<DV>(a, pw, stage, bad_tokens + 4 * (c & 1), base, r, rows, h);
             tc_fence_before();
             mbar_arrive(yd_free);
             mbar_arrive(yo_free);
             fence_proxy_async_smem();
             if (!named_bar_and(1, 128, ok)) break;         // all four warps have staged theirs, or all stop
+            if (bad && leader)                             // (the slot's next values come once it has released it, below)
+                for (int i = 0; i < 4; ++i) bad_tokens[4 * (c & 1) + i] = 0u;
             if (rows >= kBlk) {
                 if (leader) {
                     for (int x = 0; x < DV; x += 64) tma_store_3d(&maps.out, x, h, (int)base, vslot(c) + x / 64 * kHalf);

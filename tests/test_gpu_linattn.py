@@ -258,3 +258,58 @@ def test_offsets_whose_difference_overflows_touch_nothing(dtype):
     assert ssd.ssd_device_status() == 2                      # SSD_ERR_SHAPE
     assert bool((room[:32 << 20] == 77).all()) and bool((room[(32 << 20) + need:] == 77).all())
     assert bool((fin[1:] == 7.0).all())
+
+
+@pytest.mark.parametrize("dtype", [bf, f32])
+@pytest.mark.parametrize("hq,hv,dk,dv", [(1, 2, 64, 64), (2, 2, 128, 128), (1, 3, 72, 40), (1, 2, 64, 128), (1, 1, 128, 64)])
+def test_values_that_are_not_finite_reach_their_own_columns(dtype, hq, hv, dk, dv):
+    """Infinite and NaN values of a few tokens, two of them in one block and one in a block's last row:
+    their columns are not finite from those tokens on, with the value's sign in its own block (all
+    queries and keys are positive); all else is what it is without them."""
+    lens = [300, 70, 128]
+    q, k, v, ld, s0 = problem(lens, hq, hv, dk, dv, dtype, seed=21, init=True)
+    q, k = q.abs(), k.abs()
+    bad = [(0, 100, 5, float("inf")), (0, 103, 5, float("inf")), (0, 110, dv - 1, float("-inf")), (0, 127, 9, float("nan")),
+           (370, 497, 16, float("-inf")), (300, 369, 3, float("nan"))]
+    v2 = v.clone()
+    for _, t, col, x in bad:
+        v[t, 0, col], v2[t, 0, col] = x, 0.0
+    out, fin = ssd.ssd_linattn_prefill(q, k, v, ld, ref.cu(lens), scale=0.1, init_states=s0)
+    assert ssd.ssd_device_status() == 0
+    wo, wf, to, tf = ref.linattn(q, k, v2, ld, lens, 0.1, s0)
+    clean = torch.ones(out.shape, dtype=torch.bool)
+    clean_state = torch.ones(fin.shape, dtype=torch.bool)
+    for start, t, col, x in bad:
+        i = ref.offsets(lens).index(start)
+        end = start + lens[i]
+        clean[t:end, 0, col], clean_state[i, 0, :, col] = False, False
+        block = min(end, start + ((t - start) // 64 + 1) * 64)         # (64: the shorter of the two paths' blocks)
+        got = out[t:block, 0, col]
+        assert bool(torch.isnan(got).all() if x != x else (got == x).all()), (t, col)
+        assert not torch.isfinite(out[t:end, 0, col]).any() and not torch.isfinite(fin[i, 0, :, col]).any()
+    ref.assert_within(out.cpu()[clean], wo[clean], to[clean], "outputs")
+    ref.assert_within(fin.cpu()[clean_state], wf[clean_state], tf[clean_state], "states")
+
+
+@pytest.mark.parametrize("what", ["one", "inf", "nan"])
+def test_values_that_are_not_finite_cost_little(what):
+    """A block of 128 tokens takes a few microseconds; one whose values are not finite may take a
+    hundred more (128 tokens of 128 products and 128 columns in each of 128 rows: some 64,000
+    instructions a warp), not the milliseconds of forming every output anew."""
+    n = 2048
+    q, k, v, ld, _ = problem([n], 2, 4, 128, 128, bf, seed=22)
+    if what == "one":
+        v[5::128, :, 7] = float("inf")
+    else:
+        v[:] = float(what)
+    cu, best = ref.cu([n]), 1e9
+    for _ in range(4):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        out, _ = ssd.ssd_linattn_prefill(q, k, v, ld, cu)
+        b.record()
+        torch.cuda.synchronize()
+        best = min(best, a.elapsed_time(b))
+    assert ssd.ssd_device_status() == 0
+    assert not torch.isfinite(out[5:, :, 7]).any()
+    assert best < 3.0, f"{best:.3f} ms"                      # 16 blocks of 0.1 ms, and as much again
