@@ -301,6 +301,9 @@ ssd_status_t ssd_gdn_decode_step(float* state, const void* q, const void* k, con
  *          were.  Offsets that break this record SSD_ERR_SHAPE in the device error word; the
  *          outputs then mean nothing, but nothing outside the buffers is touched.
  *   out    [total_tokens][heads_v][dv] dtype (contiguous), rounded once from fp32.
+ * Inputs that are not finite stay within their sequence, head and, from their token on, the
+ * outputs that they enter.  A final state's element is infinite or NaN where the recurrence's is,
+ * as long as no power of the decay that it goes through is zero in fp32 (0 x inf is NaN).
  * `workspace` holds ssd_linattn_prefill_workspace_bytes(...) bytes of device memory.
  * Requirements: heads_v % heads_qk == 0; dk and dv multiples of 8 up to 128; heads up to
  * 65535; nseq in [1, 2^20]; total_tokens up to 2^31 - 1024; no output overlaps an input (the

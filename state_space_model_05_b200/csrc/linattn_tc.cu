@@ -59,7 +59,8 @@ __device__ __forceinline__ void fill_powers(Powers* p, float ld, int tid, int th
 }
 
 // A thread's chunk (eight elements of one token, s) of a piece of V, times w, as three bf16 parts:
-// the product's 24 bits in three cuts of 8, so that the parts' sum is exactly the fp32 product.
+// the product's 24 bits in three cuts of 8, so that the parts' sum is exactly the fp32 product.  (One
+// that is not finite leaves NaN in the lower parts: own_state.)
 __device__ __forceinline__ void split3(uint4 (&part)[3], const uint4& v, float w)
 {
     const uint32_t in[4] = {v.x, v.y, v.z, v.w};
@@ -125,6 +126,79 @@ __device__ __forceinline__ bool this_segment(const LinattnArgs& a, int blocks, c
     s->len = min(blocks * kBlk, len - s->start);
     s->first = first + s->start;
     return true;
+}
+
+// Of a bf16 number in the lower 16 bits, or of an fp32 number's upper 16.
+__device__ __forceinline__ bool not_finite(uint32_t bf16_bits) { return (bf16_bits & 0x7F80u) == 0x7F80u; }
+
+// ---- states with infinities
+// A product of an infinite value (whose lower parts are NaN) or key (which meets lower parts of zero) is
+// NaN where the recurrence has an infinity.  So where four columns of a row of U are not all finite, they
+// are formed again in fp32 on the CUDA cores, by one thread:
+//     U = sum_s g^(n-1-s) (k_s v_s^T)   over n tokens from `first`.
+// Rows and columns of the padding are zero.  Bound by the loads' latency, two tokens' at a time (four would
+// cost the output kernel's state warps registers): about 25 us for a block with one such column.
+__device__ __forceinline__ float4 own_state(const LinattnArgs& a, const Powers* pw, float ld, size_t first, int n, int h, int row, int col)
+{
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (row >= a.dk || col >= a.dv) return x;
+    const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(a.k) + first * a.k_stride + (size_t)(h / (a.hv / a.hq)) * a.dk + row;
+    const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.v) + first * a.v_stride + (size_t)h * a.dv + col;
+    constexpr int kAtOnce = 2;
+    float behind = 1.f;                                    // the decay over the whole blocks behind a token's
+    int at = -1;                                           // their number
+#pragma unroll 1
+    for (int s0 = 0; s0 < n; s0 += kAtOnce) {
+        float kk[kAtOnce];
+        uint2 y[kAtOnce];
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+            const size_t s = min(s0 + i, n - 1);
+            kk[i] = __bfloat162float(k[s * a.k_stride]);
+            y[i] = *reinterpret_cast<const uint2*>(v + s * a.v_stride);
+        }
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+            const int left = n - 1 - s0 - i;
+            if (left < 0) break;
+            if (left / kBlk != at) {
+                at = left / kBlk;
+                behind = decay_pow(ld, at * kBlk);
+            }
+            const float w = pw->up[left % kBlk] * behind;
+            x.x = fmaf(w, kk[i] * bf16lo(y[i].x), x.x);
+            x.y = fmaf(w, kk[i] * bf16hi(y[i].x), x.y);
+            x.z = fmaf(w, kk[i] * bf16lo(y[i].y), x.z);
+            x.w = fmaf(w, kk[i] * bf16hi(y[i].y), x.w);
+        }
+        if (x.x != x.x && x.y != x.y && x.z != x.z && x.w != x.w) break;
+    }
+    return x;
+}
+
+__device__ __forceinline__ bool finite4(const uint32_t (&u)[4])
+{
+    return !not_finite(u[0] >> 16) && !not_finite(u[1] >> 16) && !not_finite(u[2] >> 16) && !not_finite(u[3] >> 16);
+}
+
+// `columns` columns of U in TMEM, from `col` on, put right; a row per lane, by whole warps.
+template <int DK, int columns>
+__device__ __forceinline__ void mend_state(uint32_t tU, const LinattnArgs& a, const Powers* pw, float ld, size_t first, int n, int h, int row,
+                                           int col)
+{
+#pragma unroll 1
+    for (int c = 0; c < columns; c += 4) {
+        uint32_t u[4];
+        tmem_ld4(tU + c, u);
+        tmem_wait_ld();
+        if (row < DK && !finite4(u)) {
+            const float4 x = own_state(a, pw, ld, first, n, h, row, col + c);
+            u[0] = __float_as_uint(x.x); u[1] = __float_as_uint(x.y); u[2] = __float_as_uint(x.z); u[3] = __float_as_uint(x.w);
+        }
+        __syncwarp();
+        tmem_st4(tU + c, u);
+    }
+    tmem_wait_st();
 }
 
 // ================================================================ a segment's own state
@@ -260,8 +334,17 @@ linattn_segment_kernel(const __grid_constant__ LinattnMaps maps, const __grid_co
 #pragma unroll
             for (int q = 0; q < DV / 64; ++q) {
                 uint32_t v[16];
-                tmem_ld16(tmem + ((uint32_t)((warp & 3) * 32) << 16) + c0 + 16 * q, v);
+                const uint32_t tU = tmem + ((uint32_t)((warp & 3) * 32) << 16) + c0 + 16 * q;
+                tmem_ld16(tU, v);
                 tmem_wait_ld();
+                bool fine = true;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) fine = fine && !not_finite(v[e] >> 16);
+                if (__any_sync(0xffffffffu, row < DK && !fine)) {
+                    mend_state<DK, 16>(tU, a, pw, ld, sg.first, blocks * kBlk, h, row, c0 + 16 * q);
+                    tmem_ld16(tU, v);
+                    tmem_wait_ld();
+                }
                 if (row < DK) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
@@ -302,8 +385,6 @@ struct OutCfg {
     static constexpr uint32_t kS = 0, kYd = 128, kYo = 256, kU = 384;
 };
 
-__device__ __forceinline__ bool not_finite(uint32_t bf16_bits) { return (bf16_bits & 0x7F80u) == 0x7F80u; }
-
 // Takes the values that are not finite out of a thread's chunks of a block's tile and marks their tokens
 // (a bit each): P's zeros would not hide them from the rows before them.
 template <int DV>
@@ -314,15 +395,15 @@ __device__ __forceinline__ void take_out_bad_values(uint8_t* values, int odd, in
         int t;
         uint4* at = piece_chunk<DV>(values, p, gt, &t);
         const uint4 u = *at;
-        uint32_t w[4] = {u.x, u.y, u.z, u.w};
-        bool any = false;
+        uint32_t w[4] = {u.x, u.y, u.z, u.w}, fine = ~0u;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const bool lo = not_finite(w[j]), hi = not_finite(w[j] >> 16);
-            any |= lo || hi;
-            w[j] &= (lo ? 0u : 0xFFFFu) | (hi ? 0u : 0xFFFF0000u);
+        for (int j = 0; j < 4; ++j) {                      // x 0 = 0: all ones in a finite half
+            const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
+            const uint32_t mask = __heq2_mask(__hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w[j]), zero), zero);
+            w[j] &= mask;
+            fine &= mask;
         }
-        if (any) {
+        if (fine != ~0u) {
             *at = make_uint4(w[0], w[1], w[2], w[3]);
             atomicOr(&tokens[t >> 5], 1u << (t & 31));
         }
@@ -411,7 +492,7 @@ linattn_output_kernel(const __grid_constant__ LinattnMaps maps, const __grid_con
              *u_free = bars + 22, *conv_full = bars + 23, *conv_empty = bars + 25, *v_used = bars + 27;
     uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + L::kTm);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L::kTm + 4);
-    volatile int* bad_values = reinterpret_cast<volatile int*>(sm + L::kTm + 8);     // [4], by block mod 4
+    volatile int* bad_block = reinterpret_cast<volatile int*>(sm + L::kTm + 8);      // [4], by block mod 4: something is not finite
     unsigned* bad_tokens = reinterpret_cast<unsigned*>(sm + L::kTm + 24);            // [2][4], by block mod 2
     Powers* pw = reinterpret_cast<Powers*>(sm + L::kPow);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -454,7 +535,7 @@ linattn_output_kernel(const __grid_constant__ LinattnMaps maps, const __grid_con
             mbar_init(&conv_empty[s], 1);
         }
         *abort_flag = 0;
-        for (int i = 0; i < 4; ++i) bad_values[i] = 0;
+        for (int i = 0; i < 4; ++i) bad_block[i] = 0;
         for (int i = 0; i < 8; ++i) bad_tokens[i] = 0u;
         fence_mbar_init();
     }
@@ -481,9 +562,9 @@ linattn_output_kernel(const __grid_constant__ LinattnMaps maps, const __grid_con
     // P's zeros would not hide them.
     auto weighted_values = [&](int c, int odd, int gt) {
         const int rows = tokens(c);
-        if (!wait_warp(&v_full[c & 1], c / 2)) return false;
         const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
-        __nv_bfloat162 acc[4] = {zero, zero, zero, zero};  // NaN as soon as one of its values is not finite
+        __nv_bfloat162 acc[4] = {zero, zero, zero, zero};  // NaN as soon as one of its weighted values is not finite
+        if (!wait_warp(&v_full[c & 1], c / 2)) return false;
         uint8_t* slot = sm + L::kConv + odd * kSlot;
 #pragma unroll 1
         for (int p = odd; p < kPieces<DV>; p += 2) {
@@ -495,10 +576,10 @@ linattn_output_kernel(const __grid_constant__ LinattnMaps maps, const __grid_con
                 *at = v;
             }
             if (p * kPiece<DV> >= rows) continue;          // (the same for all threads)
-            const __nv_bfloat162* x = reinterpret_cast<const __nv_bfloat162*>(&v);
+            split3(part, v, t < rows ? pw->up[rows - 1 - t] : 0.f);
+            const __nv_bfloat162* x = reinterpret_cast<const __nv_bfloat162*>(&part[0]);
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[e] = __hfma2(x[e], zero, acc[e]);
-            split3(part, v, t < rows ? pw->up[rows - 1 - t] : 0.f);
             const int use = c * (kPieces<DV> / 2) + p / 2;
             if (use > 0 && !wait_warp(&conv_empty[odd], use - 1)) return false;
             write_piece(slot, part, gt);
@@ -515,8 +596,8 @@ linattn_output_kernel(const __grid_constant__ LinattnMaps maps, const __grid_con
             if (lane == 0) mbar_arrive(&conv_full[odd]);
         }
         const __nv_bfloat162 all = __hadd2(__hadd2(acc[0], acc[1]), __hadd2(acc[2], acc[3]));
-        if (__hisnan(all.x) || __hisnan(all.y)) {
-            bad_values[c & 3] = c + 1;
+        if (__builtin_expect(__hisnan(all.x) || __hisnan(all.y), 0)) {
+            bad_block[c & 3] = c + 1;
             take_out_bad_values<DV>(vslot(c), odd, gt, bad_tokens + 4 * (c & 1));
         }
         fence_proxy_async_smem();
@@ -622,6 +703,8 @@ linattn_output_kernel(const __grid_constant__ LinattnMaps maps, const __grid_con
                 if (!ok) break;
                 umma_commit(&k_empty[c & 1]);
                 umma_commit(&v_used[c & 1]);
+                ok = wait(&v_ok[c & 1], c / 2);            // what V~'s threads found is known before U is read
+                if (!ok) break;
                 umma_commit(u_full);
             }
             if (ok && nb > 0) wait(u_full, nb - 1);
@@ -688,6 +771,12 @@ linattn_output_kernel(const __grid_constant__ LinattnMaps maps, const __grid_con
             ok = weighted_values(c, 1, tid - kWarpState * 32) && wait_warp(u_full, c);
             if (!ok) break;
             tc_fence_after();
+            // (a key that is not finite leaves a whole row of U so: one element tells)
+            uint32_t one;
+            tmem_ld1(tmem + ((uint32_t)(quarter * 32) << 16) + L::kU + c0, one);
+            tmem_wait_ld();
+            if (__builtin_expect(bad_block[c & 3] == c + 1 || __any_sync(0xffffffffu, row < DK && not_finite(one >> 16)), 0))
+                mend_state<DK, NC>(tmem + ((uint32_t)(quarter * 32) << 16) + L::kU + c0, a, pw, ld, sg.first + (size_t)c * kBlk, tokens(c), h, row, c0);
             const float g = pw->up[tokens(c)];
 #pragma unroll
             for (int q = 0; q < NC / 16; ++q) {
@@ -764,7 +853,7 @@ linattn_output_kernel(const __grid_constant__ LinattnMaps maps, const __grid_con
             // per value slot says so, as u_full may be a block further on by now)
             ok = ok && wait_warp(yd_full, c) && wait_warp(yo_full, c) && wait_warp(&v_used[c & 1], c / 2);
             tc_fence_after();
-            const bool bad = bad_values[c & 3] == c + 1;
+            const bool bad = bad_block[c & 3] == c + 1;
             const int rows = sg.len - c * kBlk;            // rows from here on belong to another sequence
             const size_t base = sg.first + (size_t)c * kBlk;
             // the outputs go over the block's values, in the layout that they were loaded in
@@ -790,13 +879,13 @@ linattn_output_kernel(const __grid_constant__ LinattnMaps maps, const __grid_con
                         make_uint4(o[0], o[1], o[2], o[3]);
                 }
             }
-            if (bad) add_bad_values<DV>(a, pw, stage, bad_tokens + 4 * (c & 1), base, r, rows, h);
+            if (__builtin_expect(bad, 0)) add_bad_values<DV>(a, pw, stage, bad_tokens + 4 * (c & 1), base, r, rows, h);
             tc_fence_before();
             mbar_arrive(yd_free);
             mbar_arrive(yo_free);
             fence_proxy_async_smem();
             if (!named_bar_and(1, 128, ok)) break;         // all four warps have staged theirs, or all stop
-            if (bad && leader)                             // (the slot's next values come once it has released it, below)
+            if (__builtin_expect(bad && leader, 0))                             // (the slot's next values come once it has released it, below)
                 for (int i = 0; i < 4; ++i) bad_tokens[4 * (c & 1) + i] = 0u;
             if (rows >= kBlk) {
                 if (leader) {
