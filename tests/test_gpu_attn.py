@@ -308,3 +308,12 @@ def test_prefill_then_steps_is_prefill(dtype):
         outs.append(ssd.ssd_attn_decode_step(kc, vc, n, q[t:t + 1], k[t:t + 1], v[t:t + 1]))
     wo, to = ref.attn(q, k, v, [205], 0.125)
     ref.assert_within(torch.cat(outs), wo, to, "outputs")
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("hq,hkv", [(43, 1), (64, 1), (65, 1), (128, 1), (129, 1), (258, 2)])
+def test_many_query_heads_on_a_key_head(hq, hkv, dim):
+    """bf16: tiles of three tokens, of two, of one with rows to spare and of one that fills the tile; and
+    groups past 128, which run on the CUDA cores."""
+    lens = [3, 0, 130, 1, 20]
+    check(lens, *problem(sum(lens), hq, hkv, dim, bf, seed=hq), dim ** -0.5, f"{hq}/{hkv} heads of {dim}")
