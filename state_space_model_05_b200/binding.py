@@ -118,18 +118,27 @@ def _stream(stream=None):
     return stream.cuda_stream
 
 
-def _new(stream, like: torch.Tensor, shape, dtype=None, scratch=False) -> torch.Tensor:
-    """A tensor that a call on ``stream`` writes, beside ``like``.  With ``stream`` given it comes from
-    that stream's memory: the current stream's could still be read by work queued there, and a
-    workspace, dropped when the call returns, would be handed to the next call while this one runs.
-    Except for a ``scratch`` tensor, the caller may use and drop it on the current stream."""
-    if stream is None:
-        return like.new_empty(shape, dtype=dtype)
+def _made_on(stream, scratch, make, *args, **kw) -> torch.Tensor:
+    """``make(*args, **kw)``, a tensor for a call on ``stream`` to write, from that stream's memory: the
+    current stream's could still be read by work queued there, and a workspace, dropped when the call
+    returns, would be handed to the next call while this one runs.  Except for a ``scratch`` tensor,
+    the caller may use and drop it on the current stream."""
     with torch.cuda.stream(stream):
-        t = like.new_empty(shape, dtype=dtype)
+        t = make(*args, **kw)
     if not scratch:
         t.record_stream(torch.cuda.current_stream())
     return t
+
+
+def _empty(stream, like: torch.Tensor, shape, dtype, scratch=False) -> torch.Tensor:
+    """A new tensor beside ``like`` for a call on ``stream`` (None: the current one) to write."""
+    if stream is None:
+        return torch.empty(shape, device=like.device, dtype=dtype)
+    return _made_on(stream, scratch, torch.empty, shape, device=like.device, dtype=dtype)
+
+
+def _empty_like(stream, t: torch.Tensor) -> torch.Tensor:
+    return torch.empty_like(t) if stream is None else _made_on(stream, False, torch.empty_like, t)
 
 
 def _nbytes(t: torch.Tensor) -> int:
@@ -219,12 +228,12 @@ def ssd_prefill(x, dt, A, B, C, D, chunk_len, init_state=None, y=None, final_sta
                     (workspace, "workspace", workspace.shape if workspace is not None else (), None)))
     code = _dtype_code(x)
     if y is None:
-        y = _new(stream, x, x.shape)
+        y = _empty_like(stream, x)
     if final_state is None:
-        final_state = _new(stream, x, state_shape, f32)
+        final_state = _empty(stream, x, state_shape, f32)
     need = ssd_prefill_workspace_bytes(batch, seqlen, nheads, headdim, ngroups, dstate, chunk_len, code)
     if workspace is None:
-        workspace = _new(stream, x, max(need, 1), torch.uint8, scratch=True)
+        workspace = _empty(stream, x, max(need, 1), torch.uint8, scratch=True)
     if dt_softplus:
         st = lib().ssd_prefill_dtraw(_ptr(x), _ptr(dt), _ptr(dt_bias), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
                                      _ptr(init_state), batch, seqlen, nheads, headdim, ngroups, dstate,
@@ -260,13 +269,13 @@ def ssd_prefill_varlen(x, dt, A, B, C, D, cu_seqlens, chunk_len, init_states=Non
                     (workspace, "workspace", workspace.shape if workspace is not None else (), None)))
     code = _dtype_code(x)
     if y is None:
-        y = _new(stream, x, x.shape)
+        y = _empty_like(stream, x)
     if final_states is None:
-        final_states = _new(stream, x, state_shape, f32)
+        final_states = _empty(stream, x, state_shape, f32)
     need = int(lib().ssd_prefill_varlen_workspace_bytes(nseq, total, nheads, headdim, ngroups, dstate,
                                                         chunk_len, code))
     if workspace is None:
-        workspace = _new(stream, x, max(need, 1), torch.uint8, scratch=True)
+        workspace = _empty(stream, x, max(need, 1), torch.uint8, scratch=True)
     st = lib().ssd_prefill_varlen(_ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(init_states),
                                   _ptr(cu_seqlens), nseq, total, nheads, headdim, ngroups, dstate, chunk_len,
                                   code, _ptr(y), _ptr(final_states), _ptr(workspace), workspace.numel(),
@@ -290,7 +299,7 @@ def ssd_decode_step(state, x_t, dt_t, A, B_t, C_t, D, y_t=None, stream=None, dt_
                       (D, "D", (nheads,), f32), (y_t, "y_t", x_t.shape, x_t.dtype),
                       (dt_bias if dt_softplus else None, "dt_bias", (nheads,), f32)))
     if y_t is None:
-        y_t = _new(stream, x_t, x_t.shape)
+        y_t = _empty_like(stream, x_t)
     if dt_softplus:
         st = lib().ssd_decode_step_dtraw(_ptr(state), _ptr(x_t), _ptr(dt_t), _ptr(dt_bias), _ptr(A), _ptr(B_t),
                                          _ptr(C_t), _ptr(D), batch, nheads, headdim, ngroups, dstate,
@@ -317,7 +326,7 @@ def ssd_decode_steps(state, x, dt, A, B, C, D, y=None, stream=None):
                     (B, "B", B.shape, x.dtype), (C, "C", B.shape, x.dtype), (D, "D", (nheads,), f32),
                     (y, "y", x.shape, x.dtype)))
     if y is None:
-        y = _new(stream, x, x.shape)
+        y = _empty_like(stream, x)
     st = lib().ssd_decode_steps(_ptr(state), _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D), steps,
                                 batch, nheads, headdim, ngroups, dstate, _dtype_code(x), _ptr(y), _stream(stream))
     _check(st, "ssd_decode_steps")
@@ -371,7 +380,7 @@ def ssd_gdn_decode_step(state, q, k, v, gate, beta, out=None, stream=None):
                     (gate, "gate", (batch, hv), f32), (beta, "beta", (batch, hv), f32),
                     (out, "out", (batch, hv, dv), q.dtype)))
     if out is None:
-        out = _new(stream, v, v.shape)
+        out = _empty_like(stream, v)
     st = lib().ssd_gdn_decode_step(_ptr(state), _ptr(q), _ptr(k), _ptr(v), _ptr(gate), _ptr(beta), batch,
                                    hqk, hv, dk, dv, _dtype_code(q), _ptr(out), _stream(stream))
     _check(st, "ssd_gdn_decode_step")
@@ -439,12 +448,14 @@ def ssd_linattn_prefill(q, k, v, log_decay, cu_seqlens, scale=1.0, init_states=N
                   (final_states, "final_states", state_shape, f32), (workspace, "workspace", None, None)))
     code = _dtype_code(q)
     if out is None:
-        out = _new(stream, q, out_shape)
+        out = q.new_empty(out_shape) if stream is None else _made_on(stream, False, q.new_empty, out_shape)
     if final_states is None:
-        final_states = _new(stream, log_decay, state_shape)
+        final_states = (log_decay.new_empty(state_shape) if stream is None else
+                        _made_on(stream, False, log_decay.new_empty, state_shape))
     if workspace is None:
-        workspace = _new(stream, q, _workspace_bytes("ssd_linattn_prefill_workspace_bytes", nseq, total, hq, hv, dk, dv, code),
-                         torch.uint8, scratch=True)
+        need = _workspace_bytes("ssd_linattn_prefill_workspace_bytes", nseq, total, hq, hv, dk, dv, code)
+        workspace = (q.new_empty(need, dtype=torch.uint8) if stream is None else
+                     _made_on(stream, True, q.new_empty, need, dtype=torch.uint8))
     st = lib().ssd_linattn_prefill(_ptr(q), _ptr(k), _ptr(v), _packed(q), _packed(k), _packed(v), _ptr(log_decay),
                                    _ptr(init_states), _ptr(cu_seqlens), nseq, total, hq, hv, dk, dv, scale, code,
                                    _ptr(out), _ptr(final_states), _ptr(workspace), _nbytes(workspace), _stream(stream))
@@ -465,7 +476,7 @@ def ssd_linattn_decode_step(state, q, k, v, log_decay, scale=1.0, out=None, stre
                     (k, "k", key_shape, dtype), (v, "v", out_shape, dtype),
                     (log_decay, "log_decay", (hv,), f32), (out, "out", out_shape, dtype)))
     if out is None:
-        out = _new(stream, v, v.shape)
+        out = _empty_like(stream, v)
     st = lib().ssd_linattn_decode_step(_ptr(state), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), batch, hq, hv, dk, dv,
                                        scale, _dtype_code(q), _ptr(out), _stream(stream))
     _check(st, "ssd_linattn_decode_step")
@@ -487,7 +498,7 @@ def ssd_attn_prefill(q, k, v, cu_seqlens, scale=None, out=None, stream=None):
                  ((cu_seqlens, "cu_seqlens", (nseq + 1,), torch.int32), (out, "out", out_shape, q.dtype)))
     code = _dtype_code(q)
     if out is None:
-        out = _new(stream, q, out_shape)
+        out = q.new_empty(out_shape) if stream is None else _made_on(stream, False, q.new_empty, out_shape)
     st = lib().ssd_attn_prefill(_ptr(q), _ptr(k), _ptr(v), _packed(q), _packed(k), _packed(v), _ptr(cu_seqlens),
                                 nseq, total, hq, hkv, dim, dim ** -0.5 if scale is None else scale,
                                 code, _ptr(out), _stream(stream))
@@ -512,10 +523,11 @@ def ssd_attn_decode_step(k_cache, v_cache, cache_lens, q, k, v, scale=None, out=
                     (workspace, "workspace", None, None)))
     code = _dtype_code(q)
     if out is None:
-        out = _new(stream, q, q.shape)
+        out = _empty_like(stream, q)
     if workspace is None:
-        workspace = _new(stream, q, _workspace_bytes("ssd_attn_decode_workspace_bytes", batch, capacity, hq, hkv, dim, code),
-                         torch.uint8, scratch=True)
+        need = _workspace_bytes("ssd_attn_decode_workspace_bytes", batch, capacity, hq, hkv, dim, code)
+        workspace = (q.new_empty(need, dtype=torch.uint8) if stream is None else
+                     _made_on(stream, True, q.new_empty, need, dtype=torch.uint8))
     st = lib().ssd_attn_decode_step(_ptr(k_cache), _ptr(v_cache), _ptr(cache_lens), _ptr(q), _ptr(k), _ptr(v), batch,
                                     capacity, hq, hkv, dim, dim ** -0.5 if scale is None else scale, code, _ptr(out),
                                     _ptr(workspace), _nbytes(workspace), _stream(stream))
