@@ -201,6 +201,15 @@ __device__ __forceinline__ void mend_state(uint32_t tU, const LinattnArgs& a, co
     tmem_wait_st();
 }
 
+// Out of the way of the code that runs, where the registers allow a call (31 prompts of 128 x 64: 166 us with
+// it in line, 163 us so).
+template <int DK, int columns>
+__device__ __noinline__ void mend_state_apart(uint32_t tU, const LinattnArgs& a, const Powers* pw, float ld, size_t first, int n, int h,
+                                              int row, int col)
+{
+    mend_state<DK, columns>(tU, a, pw, ld, first, n, h, row, col);
+}
+
 // ================================================================ a segment's own state
 constexpr int kSegThreads = 128 + 2 * kConvThreads, kSegStages = 2, kSegSlots = 4;   // two groups take turns at the pieces
 
@@ -775,8 +784,14 @@ linattn_output_kernel(const __grid_constant__ LinattnMaps maps, const __grid_con
             uint32_t one;
             tmem_ld1(tmem + ((uint32_t)(quarter * 32) << 16) + L::kU + c0, one);
             tmem_wait_ld();
-            if (__builtin_expect(bad_block[c & 3] == c + 1 || __any_sync(0xffffffffu, row < DK && not_finite(one >> 16)), 0))
-                mend_state<DK, NC>(tmem + ((uint32_t)(quarter * 32) << 16) + L::kU + c0, a, pw, ld, sg.first + (size_t)c * kBlk, tokens(c), h, row, c0);
+            if (__builtin_expect(bad_block[c & 3] == c + 1 || __any_sync(0xffffffffu, row < DK && not_finite(one >> 16)), 0)) {
+                const uint32_t tU = tmem + ((uint32_t)(quarter * 32) << 16) + L::kU + c0;
+                const size_t base = sg.first + (size_t)c * kBlk;
+                if constexpr (NC == 32)
+                    mend_state_apart<DK, NC>(tU, a, pw, ld, base, tokens(c), h, row, c0);
+                else
+                    mend_state<DK, NC>(tU, a, pw, ld, base, tokens(c), h, row, c0);
+            }
             const float g = pw->up[tokens(c)];
 #pragma unroll
             for (int q = 0; q < NC / 16; ++q) {
