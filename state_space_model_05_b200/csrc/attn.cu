@@ -10,7 +10,8 @@
 // Bound by the fp32 units and by the shared memory that feeds them: a CTA takes 32 queries of one
 // head, a thread 4 of them with 4 (of heads over 64 dimensions: 8) output columns, in packed pairs.  Tiles of 32
 // queries rather than 64 fill the SMs with short prompts (1031 tokens, 8/2 heads of 64, two sequences:
-// 47 us a call; floor 8 us at 72 TFLOP/s).  Heads of up to 64 dimensions on the kernel for 64: 83 us for one
+// 47 us a call; floor 8 us at 72 TFLOP/s).  With ten times the tokens: 1.78 ms = 30.6 TFLOP/s, 43% of that rate,
+// as a tile's loads and products take turns between barriers.  Heads of up to 64 dimensions on the kernel for 64: 83 us for one
 // sequence of 1031, 117 us on the one for 128.
 #include "mixers.cuh"
 #include "prefill_tc.h"

@@ -20,11 +20,11 @@
 // bf16 numbers (24 bits), so that the state keeps fp32 accuracy; P and the state's image are
 // rounded to bf16 once, each by at most half the output's own rounding step.
 //
-// Bound by instructions: forming V~ (three roundings and stores per value), the masked P and the state's
-// image keep the warps issuing on half of all cycles, where a block's 128 rows of q, k, v and out would pass in
-// 0.9 us an SM.  8192 tokens, 32 heads of 128 x 128: 127 us (segment kernel 44, output kernel 96, overlapped);
-// all tensors once take 42 us.  dk and dv of up to 64 have kernels of their own: 8 x 1024 tokens, 32 heads of
-// 64 x 64: 65 us, 90 us on the ones for 128.
+// Bound by the chain of one block's steps, of which an SM has one at a time: V~, U, the state, its image, Q S,
+// the outputs.  No unit is full meanwhile (issue slots 49%, tensor pipe 25%, DRAM 32% in the output kernel):
+// the roles wait for one another.  8192 tokens, 32 heads of 128 x 128: 129 to 132 us (segment kernel 44, output
+// kernel 97, overlapped); all tensors once take 42 us.  dk and dv of up to 64 have kernels of their own: 8 x 1024
+// tokens, 32 heads of 64 x 64: 68 us, 91 us on the ones for 128.
 #include <cuda.h>
 
 #include <cmath>
@@ -940,9 +940,11 @@ linattn_output_kernel(const __grid_constant__ LinattnMaps maps, const __grid_con
 // the lengths as exponentially spread (a sequence goes on past k segments with probability
 // e^(-k len / avg), the longest of n has avg (ln n + 0.6)); a kernel then takes its work shared
 // evenly and a fifth of its longest CTA, at least that CTA.
-// Measured: 31 sequences cut at random from 16384 tokens, 32 heads: 209 us at the chosen 40 blocks, 270 us at
-// their average of 5; 1024 tokens, 8 heads: 26 us at 1, 39 us at 4; 8192 tokens, 32 heads: 128 us at 16, 194 us
-// at 4; worst found: 30 sequences of up to 300 tokens and one of 4000, 16 heads: 110 us, 100 us at 5.
+// The costs are those of 128 x 128, taken for the other sizes too.  Measured, 128 x 128 in graphs: 1024 tokens,
+// 8 heads: 23 us at the chosen 1 block, 43 us unsplit; 8192 tokens, 32 heads: 126 us at 16, 301 us unsplit; 31
+// sequences cut at random from 16384 tokens, 32 heads: 233 us at 40, 223 us unsplit.  Of 27 shapes, 13 get the
+// best of the lengths tried and 11 lose up to 11%; 64 sequences and 8 heads lose 13 to 21%, as the
+// sequences alone would fill the SMs.
 int segment_blocks(int nseq, int total, int hv)
 {
     constexpr double kOut = 2.5, kOutCta = 6, kSeg = 1.75, kSegCta = 2, kIdle = 1, kJoin = 1, kTail = 0.2;
